@@ -415,6 +415,155 @@ int moe_route_finalize(const uint16_t* x, const uint16_t* w, const float* bias, 
                        int32_t* pairs, uint8_t* q, uint8_t* scales, uint16_t* out, void* workspace,
                        size_t workspace_bytes, moe_stream_t stream);
 
+/* ===============================================================================
+ * The experts of the block in 8-bit floating point. Codes are E4M3 (4 exponent bits, 3
+ * mantissa bits, largest 448, no infinity, NaN 0x7F / 0xFF); a scale is FP32 and belongs
+ * to a block of 128 columns: of one row (activations), or of 128 rows (weights). A
+ * tensor's last block of columns or rows may be partial. nb(c) below is ceil(c / 128).
+ * The pages have no counterpart of these calls (their experts run on MXFP4 weights);
+ * the formulas are stated with each call.
+ * =============================================================================== */
+#define FP8_BLOCK 128
+
+/* -------------------------------------------------------------------------------
+ * Routing with softmax or sigmoid scores and groups of experts.
+ *   score    s[e] = 1 / (1 + exp(-x[e]))                        MOE_SCORE_SIGMOID
+ *            s[e] = exp(x[e] - max x) / sum exp(x - max x)      MOE_SCORE_SOFTMAX
+ *   key      c[e] = s[e] + bias[e]    (c = s without a bias)
+ *   groups   the E experts are n_group runs of E / n_group; a group's value is its
+ *            largest key (MOE_GROUP_MAX) or the sum of its two largest
+ *            (MOE_GROUP_TOP2); the topk_group groups of largest value (ties: the lower
+ *            group) are kept. n_group = 1 keeps everything.
+ *   choice   the K kept experts of largest key (ties: the lower expert), in that order
+ *   weight   s of the chosen, unbiased; with renormalize != 0 over their sum (0 when
+ *            the sum is 0); times scale
+ * A NaN logit has score 0 and key -infinity (below every number, chosen last), as has a
+ * NaN sum of score and bias its key; a logit of -infinity has score 0, and softmax over
+ * no logit above -infinity gives scores of 0. Under softmax the logits of +infinity
+ * share 1 equally.
+ *
+ *   logits       device, FP32 [T, E]
+ *   bias         device, FP32 [E] or NULL
+ *   ids          device, int32 [T, K]   output
+ *   weights      device, FP32 [T, K]    output, or NULL
+ *   weights_bf16 device, BF16 [T, K]    output, or NULL
+ * Requirements: T >= 0, 1 <= E <= MOE_MAX_EXPERTS, E % n_group == 0, 1 <= n_group <=
+ * MOE_MAX_GROUPS, 1 <= topk_group <= n_group, 1 <= K <= min(MOE_MAX_TOPK, topk_group *
+ * E / n_group). Sigmoid scores are moe_topk_route's bit for bit; sums and softmax are
+ * FP32 in a fixed order. Deterministic.
+ * ------------------------------------------------------------------------------- */
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SOFTMAX 1
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_TOP2 1
+#define MOE_MAX_GROUPS 64
+int moe_topk_route_grouped(const float* logits, const float* bias, int T, int E, int K, int scoring, int n_group,
+                           int topk_group, int group_rule, int renormalize, float scale, int32_t* ids, float* weights,
+                           uint16_t* weights_bf16, moe_stream_t stream);
+
+/* -------------------------------------------------------------------------------
+ * BF16 rows to E4M3 codes with one scale per row and 128 columns.
+ *   amax  = max |v| over the block, v the row's values
+ *   scale = amax / 448                                   FP8_SCALE_AMAX
+ *         = the smallest power of two >= amax / 448      FP8_SCALE_POW2
+ *   q     = E4M3( v * (448 / amax) ), or E4M3( v / scale ) for the power of two: rounded
+ *           to nearest even, saturated at +-448
+ * v is the row itself, or (fp8_block_quantize_swiglu) silu(gate) * up of a row of
+ * 2 * cols values [gate | up], silu(g) = g / (1 + exp(-g)), computed and kept in FP32.
+ * A block of zeros has scale 1; amax below 2^-110 counts as 2^-110 in the scale; a block
+ * with a NaN or an infinity has the scale NaN and every code 0x7F.
+ *
+ *   x       device, BF16, rows of `cols` (swiglu: 2 * cols) values, ldx elements apart
+ *   q       device, E4M3 [rows, cols]          output
+ *   scales  device, FP32 [rows, nb(cols)]      output
+ * Requirements: rows >= 0 (0 launches nothing), cols >= 8, cols % 8 == 0, ldx at least
+ * the row's length and ldx % 8 == 0 (MOE_ERR_INVALID_ARGUMENT); rows * nb(cols) < 2^31
+ * (MOE_ERR_CAPACITY); x 16-byte, q 8-byte, scales 4-byte aligned.
+ * ------------------------------------------------------------------------------- */
+#define FP8_SCALE_AMAX 0
+#define FP8_SCALE_POW2 1
+int fp8_block_quantize_rows(const uint16_t* x, int64_t ldx, int rows, int cols, uint8_t* q, float* scales,
+                            int scale_rule, moe_stream_t stream);
+int fp8_block_quantize_swiglu(const uint16_t* x, int64_t ldx, int rows, int cols, uint8_t* q, float* scales,
+                              int scale_rule, moe_stream_t stream);
+
+/* -------------------------------------------------------------------------------
+ * Matrix product of E4M3 codes with a scale for each block of 128.
+ *   out[m, n] = sum over blocks b of 128 columns of
+ *               a_scales[m, b] * w_scales[n / 128, b] * sum_{k in b} a[m, k] * w[n, k]
+ * Products of codes are exact; a block's sum, its scaling and the sum over blocks are
+ * FP32; out is rounded once (BF16) or not at all (FP32).
+ *
+ *   a, a_scales  device, E4M3 [M, K], FP32 [M, nb(K)]
+ *   w, w_scales  device, E4M3 [N, K], FP32 [nb(N), nb(K)]
+ *   out          device, [M, N] of out_dtype (MOE_DTYPE_F32 or MOE_DTYPE_BF16)
+ * Requirements: M >= 0, N >= 0 (either 0 launches nothing), K >= 16, K % 16 == 0
+ * (MOE_ERR_INVALID_ARGUMENT); a, w 16-byte aligned, scales 4-byte, out to its element.
+ * Deterministic.
+ * ------------------------------------------------------------------------------- */
+int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales, void* out,
+                   int out_dtype, int M, int N, int K, moe_stream_t stream);
+
+/* -------------------------------------------------------------------------------
+ * The same product for every (token, slot) pair with its own expert's weights, over the
+ * routing lists of moe_build_routing_lists.
+ * Position i of expert e's list (offsets[e] <= i < offsets[e + 1]) holds pair code
+ * p = pairs[i] (token p / topk, slot p % topk). It multiplies row
+ *   p / topk (MOE_ROWS_TOKEN), i (MOE_ROWS_LIST) or p (MOE_ROWS_PAIR)
+ * of a by expert e's weights and writes row i (MOE_ROWS_LIST) or p (MOE_ROWS_PAIR) of
+ * out. MOE_ROWS_PAIR rows of out are what moe_finalize reads without a row_index.
+ *
+ *   a, a_scales  device, E4M3 [a_rows, K], FP32 [a_rows, nb(K)]
+ *   w, w_scales  device, E4M3 [E, N, K], FP32 [E, nb(N), nb(K)]
+ *   offsets      device, int32 [E + 1]; pairs device, int32 [n_pairs]
+ *   out          device, [n_pairs, N] of out_dtype
+ * n_pairs is the length of the list (T * topk). Rows of out that no listed pair names
+ * are left as they are. A pair code outside [0, n_pairs), or an input row outside
+ * [0, a_rows), is skipped and sets MOE_DEVERR_ROW_INDEX; offsets outside [0, n_pairs]
+ * count as the nearest bound.
+ * Requirements: n_pairs >= 0, N >= 0 (either 0 launches nothing), 1 <= E <=
+ * MOE_MAX_EXPERTS, topk >= 1, a_rows >= 1; K, alignment and numerics as fp8_block_gemm.
+ * ------------------------------------------------------------------------------- */
+#define MOE_ROWS_TOKEN 0
+#define MOE_ROWS_LIST 1
+#define MOE_ROWS_PAIR 2
+int moe_expert_gemm(const uint8_t* a, const float* a_scales, int64_t a_rows, const uint8_t* w, const float* w_scales,
+                    const int32_t* offsets, const int32_t* pairs, int n_pairs, int topk, int in_rows, int out_rows,
+                    void* out, int out_dtype, int E, int N, int K, moe_stream_t stream);
+
+/* -------------------------------------------------------------------------------
+ * The norm after a block, its gate and the residual's scale, and the norm before the
+ * next block, in one pass over the rows.
+ *   u = y / sqrt(mean(y^2) + eps) * post_weight        (u = y when post_weight is NULL)
+ *   h = residual + alpha * (gate * u)                   (no gate: alpha * u)
+ *   n = h / sqrt(mean(h^2) + eps) * next_weight
+ * in FP32; h is rounded once to residual_dtype and n once to BF16. n is made from h
+ * before its rounding, and the codes (q, scales: fp8_block_quantize_rows' with the rule
+ * FP8_SCALE_AMAX) from n before its own.
+ *
+ *   y            device, BF16, rows of H values, ldy elements apart (the block's output)
+ *   residual     device, [T, H] of residual_dtype (MOE_DTYPE_F32 or MOE_DTYPE_BF16)
+ *   post_weight  device, BF16 [H] or NULL
+ *   gate         device, BF16 [T] (MOE_GATE_TOKEN), [H] (MOE_GATE_CHANNEL), [T, H]
+ *                (MOE_GATE_FULL), or NULL with MOE_GATE_NONE
+ *   next_weight  device, BF16 [H]
+ *   h            device, [T, H] of residual_dtype   output; may be `residual` itself
+ *   n            device, BF16 [T, H]                output, or NULL
+ *   q, scales    device, E4M3 [T, H], FP32 [T, nb(H)]   outputs, or both NULL
+ * Requirements: T >= 0 (0 launches nothing), 8 <= H, H % 8 == 0, ldy >= H, ldy % 8 ==
+ * 0, eps >= 0 (MOE_ERR_INVALID_ARGUMENT), H <= 16384 (MOE_ERR_CAPACITY); y, residual,
+ * h, n, the weights and a channel or full gate 16-byte aligned, q 8-byte, scales 4-byte,
+ * a token gate 2-byte. Sums are FP32 in a fixed order. Deterministic.
+ * ------------------------------------------------------------------------------- */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_TOKEN 1
+#define MOE_GATE_CHANNEL 2
+#define MOE_GATE_FULL 3
+int moe_block_norm(const uint16_t* y, int64_t ldy, const void* residual, int residual_dtype,
+                   const uint16_t* post_weight, const uint16_t* gate, int gate_kind, const uint16_t* next_weight,
+                   float alpha, float eps, int T, int H, void* h, uint16_t* n, uint8_t* q, float* scales,
+                   moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

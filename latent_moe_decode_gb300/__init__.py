@@ -24,6 +24,9 @@ __all__ = [
     "finalize", "finalize_rmsnorm", "route_finalize", "route_finalize_workspace", "device_error", "RouteFinalize",
     "ROUTER_AUTO", "ROUTER_SIMT", "ROUTER_TCGEN05", "MXFP8_SCALE_FLOOR", "MXFP8_SCALE_CEIL",
     "DEVERR_ROW_INDEX", "DEVERR_EXPERT_ID", "DEVERR_TIMEOUT", "DEVERR_CAPACITY",
+    "topk_route_grouped", "fp8_block_quantize_rows", "fp8_block_quantize_swiglu", "fp8_block_gemm", "expert_gemm",
+    "block_norm", "FP8_BLOCK", "SCORE_SIGMOID", "SCORE_SOFTMAX", "GROUP_MAX", "GROUP_TOP2", "FP8_SCALE_AMAX",
+    "FP8_SCALE_POW2", "ROWS_TOKEN", "ROWS_LIST", "ROWS_PAIR",
 ]
 
 OK, ERR_INVALID_ARGUMENT, ERR_ALIGNMENT, ERR_CAPACITY, ERR_WORKSPACE, ERR_UNSUPPORTED, ERR_CUDA = range(7)
@@ -31,9 +34,15 @@ DEVERR_ROW_INDEX, DEVERR_EXPERT_ID, DEVERR_TIMEOUT, DEVERR_CAPACITY = 0x1, 0x2, 
 ROUTER_AUTO, ROUTER_SIMT, ROUTER_TCGEN05 = 0, 1, 2
 MXFP8_SCALE_FLOOR, MXFP8_SCALE_CEIL = 0, 1
 DTYPE_F32, DTYPE_BF16 = 0, 1
+FP8_BLOCK = 128
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+FP8_SCALE_AMAX, FP8_SCALE_POW2 = 0, 1
+ROWS_TOKEN, ROWS_LIST, ROWS_PAIR = 0, 1, 2
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = 0, 1, 2, 3
 
 # Every symbol the header declares, with its ctypes signature.
-_P, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_P, _I, _SZ, _F, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_int64
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_version": (_I, []),
@@ -58,6 +67,12 @@ SIGNATURES = {
     "moe_finalize_rmsnorm": (_I, [_P, ctypes.c_int64, _P, _P, _I, _F, _P, _F, _I, _I, _I, _P, _P, _P]),
     "moe_route_finalize_workspace": (_SZ, [_I, _I, _I, _I]),
     "moe_route_finalize": (_I, [_P] * 5 + [_I] * 6 + [_F] + [_P] * 9 + [_P, _SZ, _P]),
+    "moe_topk_route_grouped": (_I, [_P, _P] + [_I] * 8 + [_F, _P, _P, _P, _P]),
+    "fp8_block_quantize_rows": (_I, [_P, _L, _I, _I, _P, _P, _I, _P]),
+    "fp8_block_quantize_swiglu": (_I, [_P, _L, _I, _I, _P, _P, _I, _P]),
+    "fp8_block_gemm": (_I, [_P] * 5 + [_I] * 4 + [_P]),
+    "moe_expert_gemm": (_I, [_P, _P, _L, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P]),
+    "moe_block_norm": (_I, [_P, _L, _P, _I, _P, _P, _I, _P, _F, _F, _I, _I, _P, _P, _P, _P, _P]),
 }
 
 _lib = None
@@ -371,6 +386,158 @@ def route_finalize(x, w, bias, latent, rows, K: int, renormalize: bool, scale: f
         _ptr(logits), _ptr(ids), _ptr(weights), _ptr(weights_bf16), _ptr(offsets), _ptr(pairs), _ptr(q), _ptr(scales),
         _ptr(out), _ptr(workspace), ws, _stream(stream)))
     return out
+
+
+# --- the experts in 8-bit floating point: E4M3 codes (torch.uint8) with an FP32 scale per
+# --- row and 128 columns (activations) or per 128 x 128 block (weights)
+def _rows_2d(t, dtype, name):
+    """A 2-D CUDA tensor of contiguous rows, `stride(0)` elements apart (a slice of wider rows is one)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected two dimensions and contiguous rows")
+    return t
+
+
+def _row_stride(t):
+    """Elements between rows (a single row has any stride: its length then)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def _out_dtype(out, out_dtype):
+    dt = out.dtype if out is not None else out_dtype
+    if dt == torch.bfloat16:
+        return dt, DTYPE_BF16
+    if dt == torch.float32:
+        return dt, DTYPE_F32
+    raise TypeError("out: expected float32 or bfloat16")
+
+
+def topk_route_grouped(logits, bias, K: int, n_group: int = 1, topk_group: int = 1, scoring: int = SCORE_SIGMOID,
+                       group_rule: int = GROUP_TOP2, renormalize: bool = True, scale: float = 1.0, ids=None,
+                       weights=None, weights_bf16=None, want_bf16: bool = True, stream=None):
+    """(ids int32 [T,K], weights FP32 [T,K], weights BF16 [T,K] or None): sigmoid or softmax
+    scores, the choice among the best topk_group of n_group groups of experts."""
+    T, E = logits.shape
+    _need(logits, torch.float32, (T, E), "logits")
+    if bias is not None:
+        _need(bias, torch.float32, (E,), "bias")
+    ids = _empty((T, K), torch.int32, logits) if ids is None else _need(ids, torch.int32, (T, K), "ids")
+    weights = _empty((T, K), torch.float32, logits) if weights is None else _need(weights, torch.float32, (T, K), "weights")
+    if weights_bf16 is not None:
+        _need(weights_bf16, torch.bfloat16, (T, K), "weights_bf16")
+    elif want_bf16:
+        weights_bf16 = _empty((T, K), torch.bfloat16, logits)
+    _check("moe_topk_route_grouped", load().moe_topk_route_grouped(
+        _ptr(logits), _ptr(bias), T, E, K, int(scoring), int(n_group), int(topk_group), int(group_rule),
+        int(bool(renormalize)), float(scale), _ptr(ids), _ptr(weights), _ptr(weights_bf16), _stream(stream)))
+    return ids, weights, weights_bf16
+
+
+def _block_quantize(fn, x, cols, q, scales, scale_rule, stream):
+    rows = x.shape[0]
+    q = _empty((rows, cols), torch.uint8, x) if q is None else _need(q, torch.uint8, (rows, cols), "q")
+    nb = _blocks(cols)
+    scales = _empty((rows, nb), torch.float32, x) if scales is None else _need(scales, torch.float32, (rows, nb), "scales")
+    _check(fn, getattr(load(), fn)(_ptr(x), _row_stride(x), rows, cols, _ptr(q), _ptr(scales), int(scale_rule),
+                                   _stream(stream)))
+    return q, scales
+
+
+def fp8_block_quantize_rows(x, q=None, scales=None, scale_rule: int = FP8_SCALE_AMAX, stream=None):
+    """(E4M3 codes uint8 [rows, cols], FP32 scales [rows, ceil(cols / 128)]) of BF16 rows
+    (contiguous rows; their stride may exceed their length)."""
+    _rows_2d(x, torch.bfloat16, "x")
+    return _block_quantize("fp8_block_quantize_rows", x, x.shape[1], q, scales, scale_rule, stream)
+
+
+def fp8_block_quantize_swiglu(gate_up, q=None, scales=None, scale_rule: int = FP8_SCALE_AMAX, stream=None):
+    """The codes and scales of silu(gate) * up [rows, F], gate_up BF16 [rows, 2 F] = [gate | up]."""
+    _rows_2d(gate_up, torch.bfloat16, "gate_up")
+    if gate_up.shape[1] % 2:
+        raise ValueError("gate_up: expected an even number of columns")
+    return _block_quantize("fp8_block_quantize_swiglu", gate_up, gate_up.shape[1] // 2, q, scales, scale_rule, stream)
+
+
+def fp8_block_gemm(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16, stream=None):
+    """out [M, N] (BF16 or FP32) = codes a [M, K] times codes w [N, K]^T with their scales
+    (a_scales FP32 [M, ceil(K/128)], w_scales FP32 [ceil(N/128), ceil(K/128)])."""
+    M, K = a.shape
+    N = w.shape[0]
+    _need(a, torch.uint8, (M, K), "a")
+    _need(a_scales, torch.float32, (M, _blocks(K)), "a_scales")
+    _need(w, torch.uint8, (N, K), "w")
+    _need(w_scales, torch.float32, (_blocks(N), _blocks(K)), "w_scales")
+    dt, code = _out_dtype(out, out_dtype)
+    out = _empty((M, N), dt, a) if out is None else _need(out, dt, (M, N), "out")
+    _check("fp8_block_gemm", load().fp8_block_gemm(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(out), code,
+                                                   M, N, K, _stream(stream)))
+    return out
+
+
+def expert_gemm(a, a_scales, w, w_scales, offsets, pairs, topk: int, in_rows: int = ROWS_TOKEN,
+                out_rows: int = ROWS_PAIR, out=None, out_dtype=torch.bfloat16, stream=None):
+    """out [n_pairs, N] (BF16 or FP32): every listed pair's row of codes a times its expert's
+    weights w [E, N, K]^T, over the lists of build_routing_lists (offsets [E+1], pairs).
+    in_rows: which row of a a pair multiplies (ROWS_TOKEN, ROWS_LIST, ROWS_PAIR); out_rows:
+    which row of out it writes (ROWS_LIST, ROWS_PAIR)."""
+    a_rows, K = a.shape
+    E, N = w.shape[0], w.shape[1]
+    P = pairs.shape[0]
+    _need(a, torch.uint8, (a_rows, K), "a")
+    _need(a_scales, torch.float32, (a_rows, _blocks(K)), "a_scales")
+    _need(w, torch.uint8, (E, N, K), "w")
+    _need(w_scales, torch.float32, (E, _blocks(N), _blocks(K)), "w_scales")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    _need(pairs, torch.int32, (P,), "pairs")
+    dt, code = _out_dtype(out, out_dtype)
+    out = _empty((P, N), dt, a) if out is None else _need(out, dt, (P, N), "out")
+    _check("moe_expert_gemm", load().moe_expert_gemm(
+        _ptr(a), _ptr(a_scales), a_rows, _ptr(w), _ptr(w_scales), _ptr(offsets), _ptr(pairs), P, int(topk), int(in_rows),
+        int(out_rows), _ptr(out), code, E, N, K, _stream(stream)))
+    return out
+
+
+def block_norm(y, residual, next_weight, post_weight=None, gate=None, alpha: float = 1.0, eps: float = 1e-6, h=None,
+               n=None, quantize: bool = False, q=None, scales=None, stream=None):
+    """(h, n, q, scales): h = residual + alpha * gate * rms(y) * post_weight (of the residual's
+    dtype, BF16 or FP32), n = rms(h) * next_weight (BF16), and with quantize n's codes and
+    scales (else None). gate: BF16 [T, 1], [H] or [T, H]. h may be the residual itself."""
+    T, H = residual.shape
+    _rows_2d(y, torch.bfloat16, "y")
+    if tuple(y.shape) != (T, H):
+        raise ValueError(f"y: expected shape {(T, H)}, got {tuple(y.shape)}")
+    dt, code = _out_dtype(residual, None)
+    _need(residual, dt, (T, H), "residual")
+    _need(next_weight, torch.bfloat16, (H,), "next_weight")
+    if post_weight is not None:
+        _need(post_weight, torch.bfloat16, (H,), "post_weight")
+    kind = GATE_NONE
+    if gate is not None:
+        _need(gate, torch.bfloat16, None, "gate")
+        kind = {(T, H): GATE_FULL, (H,): GATE_CHANNEL, (T, 1): GATE_TOKEN}.get(tuple(gate.shape))
+        if kind is None:
+            raise ValueError(f"gate: expected shape {(T, 1)}, {(H,)} or {(T, H)}, got {tuple(gate.shape)}")
+    h = _empty((T, H), dt, y) if h is None else _need(h, dt, (T, H), "h")
+    n = _empty((T, H), torch.bfloat16, y) if n is None else _need(n, torch.bfloat16, (T, H), "n")
+    if quantize:
+        q = _empty((T, H), torch.uint8, y) if q is None else _need(q, torch.uint8, (T, H), "q")
+        nb = _blocks(H)
+        scales = _empty((T, nb), torch.float32, y) if scales is None else _need(scales, torch.float32, (T, nb), "scales")
+    else:
+        q = scales = None
+    _check("moe_block_norm", load().moe_block_norm(
+        _ptr(y), _row_stride(y), _ptr(residual), code, _ptr(post_weight), _ptr(gate), kind, _ptr(next_weight),
+        float(alpha), float(eps), T, H, _ptr(h), _ptr(n), _ptr(q), _ptr(scales), _stream(stream)))
+    return h, n, q, scales
 
 
 class RouteFinalize:

@@ -1,0 +1,181 @@
+// The norm after a block, its gate and the residual's scale, and the norm before the
+// next block, in one pass over the rows:
+//   u = y / sqrt(mean(y^2) + eps) * post_weight
+//   h = residual + alpha * (gate * u)
+//   n = h / sqrt(mean(h^2) + eps) * next_weight      (and n's E4M3 codes)
+//
+// Bound by HBM: each row of y, residual and gate is read once and h, n and the codes
+// written once. One CTA per row holds the row in registers (8 consecutive columns per
+// 16-byte fragment, up to kV fragments a thread), so both sums of squares -- each
+// thread's columns in order, a shuffle tree, the warps in order -- and all outputs come
+// from one load. 16 consecutive lanes hold one block of 128 columns for the codes.
+#include "fp8_block.cuh"
+
+namespace moe {
+namespace {
+
+using namespace fp8_impl;
+
+constexpr int kMaxThreads = 512;
+constexpr int kMaxH = 16384;
+
+struct BlockNormArgs {
+  const uint16_t* y;
+  long long ldy;
+  const void* residual;
+  const uint16_t *post, *gate, *next;
+  float alpha, eps;
+  int H, nb;
+  void* h;
+  uint16_t* n;
+  uint8_t* q;
+  float* scales;
+};
+
+// The CTA's sum of one value per thread, in a fixed order, for every thread.
+__device__ __forceinline__ float cta_sum(float v, float* slots) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFullMask, v, o));
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s = __fadd_rn(s, slots[w]);
+  return s;
+}
+
+template <int V, bool F32, int GATE>
+__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNormArgs a) {
+  __shared__ float slots[2][kMaxThreads / 32];
+  grid_launch_dependents();
+  grid_wait();
+  const long long row = blockIdx.x;
+  const int nv = a.H / 8;  // fragments of the row
+  float y[V][8], r[V][8];
+  uint4 g[V];
+  const uint16_t* yr = a.y + row * a.ldy;
+  const long long at = row * a.H;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int f = i * blockDim.x + threadIdx.x;
+    const bool in = f < nv;
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    bf16x8_to_f32(in ? ld_nc16(yr + 8 * f) : z, y[i]);
+    if (F32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + at + 8 * f);
+      const float4 lo = in ? p[0] : make_float4(0, 0, 0, 0), hi = in ? p[1] : make_float4(0, 0, 0, 0);
+      r[i][0] = lo.x, r[i][1] = lo.y, r[i][2] = lo.z, r[i][3] = lo.w;
+      r[i][4] = hi.x, r[i][5] = hi.y, r[i][6] = hi.z, r[i][7] = hi.w;
+    } else {  // (not the read-only path: h may be written over the residual)
+      bf16x8_to_f32(in ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + at + 8 * f) : z, r[i]);
+    }
+    if (GATE == MOE_GATE_FULL) g[i] = in ? ld_nc16(a.gate + at + 8 * f) : z;
+    if (GATE == MOE_GATE_CHANNEL) g[i] = in ? ld_nc16(a.gate + 8 * f) : z;
+  }
+  float root = 1.f;
+  if (a.post) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = __fmaf_rn(y[i][j], y[i][j], ss);
+    root = __frsqrt_rn(__fadd_rn(__fdiv_rn(cta_sum(ss, slots[0]), (float)a.H), a.eps));
+  }
+  const float tg = GATE == MOE_GATE_TOKEN ? bf16_to_f32(a.gate[row]) : 1.f;
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int f = i * blockDim.x + threadIdx.x;
+    float p[8], gv[8];
+    if (a.post) bf16x8_to_f32(f < nv ? ld_nc16(a.post + 8 * f) : make_uint4(0, 0, 0, 0), p);
+    if (GATE == MOE_GATE_FULL || GATE == MOE_GATE_CHANNEL) bf16x8_to_f32(g[i], gv);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float u = y[i][j];
+      if (a.post) u = __fmul_rn(__fmul_rn(u, root), p[j]);
+      if (GATE == MOE_GATE_TOKEN) u = __fmul_rn(u, tg);
+      if (GATE == MOE_GATE_FULL || GATE == MOE_GATE_CHANNEL) u = __fmul_rn(u, gv[j]);
+      r[i][j] = __fmaf_rn(a.alpha, u, r[i][j]);
+      ss = __fmaf_rn(r[i][j], r[i][j], ss);
+    }
+    if (f < nv) {
+      if (F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.h) + at + 8 * f);
+        o[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
+        o[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+      } else {
+        st16(static_cast<uint16_t*>(a.h) + at + 8 * f,
+             make_uint4(pack_bf16x2(r[i][0], r[i][1]), pack_bf16x2(r[i][2], r[i][3]), pack_bf16x2(r[i][4], r[i][5]),
+                        pack_bf16x2(r[i][6], r[i][7])));
+      }
+    }
+  }
+  root = __frsqrt_rn(__fadd_rn(__fdiv_rn(cta_sum(ss, slots[1]), (float)a.H), a.eps));
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int f = i * blockDim.x + threadIdx.x;
+    float w[8];
+    bf16x8_to_f32(f < nv ? ld_nc16(a.next + 8 * f) : make_uint4(0, 0, 0, 0), w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(__fmul_rn(r[i][j], root), w[j]);
+    if (a.n && f < nv)
+      st16(a.n + at + 8 * f, make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]),
+                                        pack_bf16x2(w[6], w[7])));
+    if (a.q) {
+      if (f >= nv) {  // (0 * infinity past the row's end)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0.f;
+      }
+      const BlockScale s = block_scale<false>(block_max(magnitude(w)));
+      if (f < nv) {
+        *reinterpret_cast<uint2*>(a.q + at + 8 * f) = encode8(w, s);
+        if ((f & 15) == 0) a.scales[row * a.nb + (f >> 4)] = s.scale;
+      }
+    }
+  }
+}
+
+template <int V, bool F32>
+int launch_gate(int kind, const BlockNormArgs& a, int T, int threads, cudaStream_t s) {
+  switch (kind) {
+    case MOE_GATE_TOKEN: return launch_pdl(block_norm_kernel<V, F32, MOE_GATE_TOKEN>, dim3(T), dim3(threads), 0, s, a);
+    case MOE_GATE_CHANNEL: return launch_pdl(block_norm_kernel<V, F32, MOE_GATE_CHANNEL>, dim3(T), dim3(threads), 0, s, a);
+    case MOE_GATE_FULL: return launch_pdl(block_norm_kernel<V, F32, MOE_GATE_FULL>, dim3(T), dim3(threads), 0, s, a);
+    default: return launch_pdl(block_norm_kernel<V, F32, MOE_GATE_NONE>, dim3(T), dim3(threads), 0, s, a);
+  }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_block_norm(const uint16_t* y, int64_t ldy, const void* residual, int residual_dtype,
+                              const uint16_t* post_weight, const uint16_t* gate, int gate_kind,
+                              const uint16_t* next_weight, float alpha, float eps, int T, int H, void* h, uint16_t* n,
+                              uint8_t* q, float* scales, moe_stream_t stream) {
+  using namespace moe;
+  if (T < 0 || H < 8 || H % 8 != 0 || ldy < H || ldy % 8 != 0 || !(eps >= 0.f)) return MOE_ERR_INVALID_ARGUMENT;
+  if (residual_dtype != MOE_DTYPE_F32 && residual_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+  if (gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_FULL || (gate_kind != MOE_GATE_NONE) != (gate != nullptr))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if ((q == nullptr) != (scales == nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+  if (H > kMaxH) return MOE_ERR_CAPACITY;
+  if (T == 0) return MOE_OK;
+  if (!y || !residual || !next_weight || !h) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(y, 16) || !aligned(residual, 16) || !aligned(h, 16) || !aligned(next_weight, 16) ||
+      !aligned(post_weight, 16) || !aligned(n, 16) || !aligned(q, 8) || !aligned(scales, 4) ||
+      !aligned(gate, gate_kind == MOE_GATE_TOKEN ? 2 : 16))
+    return MOE_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  int st = current_device(&dev);
+  if (st != MOE_OK) return st;
+  BlockNormArgs a;
+  a.y = y, a.ldy = ldy, a.residual = residual, a.post = post_weight, a.gate = gate, a.next = next_weight;
+  a.alpha = alpha, a.eps = eps, a.H = H, a.nb = (H + FP8_BLOCK - 1) / FP8_BLOCK;
+  a.h = h, a.n = n, a.q = q, a.scales = scales;
+  const int nv = H / 8, v = nv <= kMaxThreads ? 1 : (nv <= 2 * kMaxThreads ? 2 : 4);
+  const int threads = ((nv + v - 1) / v + 31) / 32 * 32;
+  const cudaStream_t s = as_cuda(stream);
+  const bool f32 = residual_dtype == MOE_DTYPE_F32;
+  if (v == 1) return f32 ? launch_gate<1, true>(gate_kind, a, T, threads, s) : launch_gate<1, false>(gate_kind, a, T, threads, s);
+  if (v == 2) return f32 ? launch_gate<2, true>(gate_kind, a, T, threads, s) : launch_gate<2, false>(gate_kind, a, T, threads, s);
+  return f32 ? launch_gate<4, true>(gate_kind, a, T, threads, s) : launch_gate<4, false>(gate_kind, a, T, threads, s);
+}

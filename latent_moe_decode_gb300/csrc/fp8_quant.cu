@@ -1,0 +1,99 @@
+// BF16 rows (or silu(gate) * up of [gate | up] rows) to E4M3 codes with one FP32 scale
+// per row and 128 columns.
+//
+// Per block: amax = max |v|, scale = amax / 448 (or the smallest power of two at or
+// above it), q = E4M3(v * 448 / amax). Bound by HBM: 2 (swiglu: 4) bytes in and 1 + 1/32
+// out per value.
+//
+// A block is 16 lanes with one 16-byte load each (two with swiglu), its maximum four
+// xor-shuffles away, so nothing is read twice and nothing staged. A warp takes two
+// consecutive blocks of the [rows, blocks] order: 512 contiguous bytes a load, 256 a
+// store.
+#include "fp8_block.cuh"
+
+namespace moe {
+namespace {
+
+using namespace fp8_impl;
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // blocks a half-warp has in flight
+
+template <bool SWIGLU, bool POW2>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __restrict__ x, long long ldx, int cols,
+                                                            int nb, int units, uint8_t* __restrict__ q,
+                                                            float* __restrict__ scales) {
+  grid_launch_dependents();
+  grid_wait();
+  const int l = threadIdx.x & 15;
+  const int half = (int)((blockIdx.x * kThreads + threadIdx.x) >> 4), halves = (int)(gridDim.x * kThreads) >> 4;
+  // (a warp's two half-warps leave the loop together: the shuffles are warp-wide)
+  for (int u0 = half; (u0 & ~1) < units; u0 += halves * kUnroll) {
+    uint4 a[kUnroll], b[kUnroll];
+    int row[kUnroll], col[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int u = u0 + i * halves;
+      row[i] = u / nb;
+      col[i] = (u - row[i] * nb) * FP8_BLOCK + 8 * l;
+      const bool in = u >= 0 && u < units && col[i] < cols;
+      if (!in) col[i] = -1;
+      const uint16_t* p = x + (long long)row[i] * ldx + col[i];
+      a[i] = in ? ld_nc16(p) : make_uint4(0, 0, 0, 0);
+      if (SWIGLU) b[i] = in ? ld_nc16(p + cols) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int u = u0 + i * halves;
+      float v[8];
+      bf16x8_to_f32(a[i], v);
+      if (SWIGLU) {
+        float up[8];
+        bf16x8_to_f32(b[i], up);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fdiv_rn(v[j], 1.f + expf(-v[j])), up[j]);
+      }
+      const BlockScale s = block_scale<POW2>(block_max(magnitude(v)));
+      if (col[i] >= 0) {
+        *reinterpret_cast<uint2*>(q + (long long)row[i] * cols + col[i]) = encode8(v, s);
+        if (l == 0) scales[u] = s.scale;
+      }
+    }
+  }
+}
+
+int quantize(const uint16_t* x, int64_t ldx, int rows, int cols, uint8_t* q, float* scales, int scale_rule, bool swiglu,
+             cudaStream_t stream) {
+  if (rows < 0 || cols < 8 || cols % 8 != 0 || cols > (1 << 29)) return MOE_ERR_INVALID_ARGUMENT;
+  if (scale_rule != FP8_SCALE_AMAX && scale_rule != FP8_SCALE_POW2) return MOE_ERR_INVALID_ARGUMENT;
+  if (ldx < (swiglu ? 2LL * cols : (long long)cols) || ldx % 8 != 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scales) return MOE_ERR_INVALID_ARGUMENT;
+  const int nb = (cols + FP8_BLOCK - 1) / FP8_BLOCK;
+  if ((long long)rows * nb >= (1LL << 31) - (1LL << 24)) return MOE_ERR_CAPACITY;  // (the loop's index passes the end)
+  if (!aligned(x, 16) || !aligned(q, 8) || !aligned(scales, 4)) return MOE_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  int st = current_device(&dev);
+  if (st != MOE_OK) return st;
+  const int units = rows * nb;
+  const long long need = ((long long)units + kThreads / 16 - 1) / (kThreads / 16);
+  const long long most = 8LL * dev.sm_count;
+  const bool p2 = scale_rule == FP8_SCALE_POW2;
+  auto kern = swiglu ? (p2 ? quantize_kernel<true, true> : quantize_kernel<true, false>)
+                     : (p2 ? quantize_kernel<false, true> : quantize_kernel<false, false>);
+  return launch_pdl(kern, dim3((unsigned)(need < most ? need : most)), dim3(kThreads), 0, stream, x, (long long)ldx,
+                    cols, nb, units, q, scales);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int fp8_block_quantize_rows(const uint16_t* x, int64_t ldx, int rows, int cols, uint8_t* q, float* scales,
+                                       int scale_rule, moe_stream_t stream) {
+  return moe::quantize(x, ldx, rows, cols, q, scales, scale_rule, false, moe::as_cuda(stream));
+}
+
+extern "C" int fp8_block_quantize_swiglu(const uint16_t* x, int64_t ldx, int rows, int cols, uint8_t* q, float* scales,
+                                         int scale_rule, moe_stream_t stream) {
+  return moe::quantize(x, ldx, rows, cols, q, scales, scale_rule, true, moe::as_cuda(stream));
+}
