@@ -25,7 +25,8 @@ int launch(GemmArgs& a, cudaStream_t stream) {
   int st = current_device(&dev);
   if (st != MOE_OK) return st;
   a.err = dev.error_word;
-  return fp8_impl::launch_narrow(a, dev.sm_count, stream);
+  const bool wide = a.offsets ? (long long)a.M >= 96LL * a.E : a.M >= 256;
+  return wide ? fp8_impl::launch_wide(a, dev.sm_count, stream) : fp8_impl::launch_narrow(a, dev.sm_count, stream);
 }
 
 }  // namespace

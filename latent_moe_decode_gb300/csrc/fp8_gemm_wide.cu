@@ -1,0 +1,385 @@
+// Block-128 E4M3 product for many rows per weight tile (prompts, experts with hundreds of
+// rows): rows on the tensor core's lanes, weights on its columns, two SMs per tile.
+//
+// Bound by the tensor cores. A pair of CTAs runs one M = 256, N = 256 MMA (cta_group::2)
+// over 256 rows of a (128 lanes of each CTA) and 256 weight rows (128 staged by each), so
+// an SM stages 32 KB per block of 128 columns for 512 cycles of multiplication: half of
+// what two single CTAs would draw from L2 for the same work. A block's sum stays in one
+// of two TMEM slots of 256 columns; with the rows on the lanes a thread's scale is one
+// number for 128 columns:
+//   - warps 0-15: epilogue. Warp w reads lanes 32 (w % 4).. and columns 64 (w / 4)..,
+//     and folds each block's sums, times sa sw, into 64 FP32 registers a thread;
+//   - warp 16: TMA producer (rows of an expert's list by gather4, four at a time);
+//   - warp 17: MMA issuer (in the pair's even CTA, for both);
+//   - warp 18: scales. It walks the rows' scales ahead of the epilogue and leaves the
+//     products sa sw of a block, for both weight blocks of the tile, in a ring in shared
+//     memory, so that the row-major scales are fetched once per CTA and not per warp.
+// A persistent grid of pairs walks the tiles, row tiles of the same weights side by side.
+#include "fp8_gemm.cuh"
+
+namespace moe {
+namespace fp8_impl {
+namespace {
+
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 32 * (kEpiWarps + 3);
+constexpr int kRows = 256, kCols = 256;       // a pair's tile
+constexpr int kHalf = 128 * FP8_BLOCK;        // bytes of one CTA's rows, or weights, of a stage
+constexpr int kStageBytes = 2 * kHalf;
+constexpr int kMaxStages = 6;
+constexpr int kSlots = 2;                     // TMEM accumulators: all 512 columns
+constexpr int kScaleSlots = 4;
+constexpr int kScaleBytes = kScaleSlots * 2 * 128 * 4;
+
+struct Tile {
+  int e, n0, pos, cnt;  // expert, first weight row, this CTA's first row and its rows (may be <= 0)
+};
+
+template <bool GROUPED>
+__device__ __forceinline__ Tile tile_at(const GemmArgs& g, const int* table, int t, int half) {
+  Tile r;
+  const int nt = (g.nbn + 1) / 2;
+  if constexpr (GROUPED) {
+    r.e = tile_expert(table, g.E, t / nt);
+    const int c = table[r.e + 1] - table[r.e], local = t - table[r.e] * nt;
+    const int lo = clamp_offset(__ldg(g.offsets + r.e), g.M), hi = clamp_offset(__ldg(g.offsets + r.e + 1), g.M);
+    r.n0 = local / c * kCols;
+    r.pos = lo + local % c * kRows + half * 128;
+    r.cnt = min(128, hi - r.pos);
+  } else {
+    const int mt = (g.M - 1) / kRows + 1;
+    r.e = 0;
+    r.n0 = t / mt * kCols;
+    r.pos = t % mt * kRows + half * 128;
+    r.cnt = min(128, g.M - r.pos);
+  }
+  return r;
+}
+
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc));
+}
+
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* map, int c0, int r0, int r1, int r2,
+                                                 int r3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+      "%3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
+
+// Arrive on a barrier of the cluster (a shared::cluster address).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// 64 outputs of one row from column n on: whole 32-byte sectors a store where the rows
+// are so aligned and the columns all exist (vec), else one by one.
+__device__ __forceinline__ void store_row(const GemmArgs& g, long long row, int n, const uint64_t (&acc)[32], bool vec) {
+  if (g.f32) {
+    float* o = static_cast<float*>(g.out) + row * g.N + n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float lo, hi;
+        unpack2(acc[4 * i + j], &lo, &hi);
+        v[2 * j] = __float_as_uint(lo), v[2 * j + 1] = __float_as_uint(hi);
+      }
+      if (vec) {
+        st32(o + 8 * i, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (n + 8 * i + j < g.N) o[8 * i + j] = __uint_as_float(v[j]);
+      }
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(g.out) + row * g.N + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float lo, hi;
+        unpack2(acc[8 * i + j], &lo, &hi);
+        v[j] = pack_bf16x2(lo, hi);
+      }
+      if (vec) {
+        st32(o + 16 * i, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (n + 16 * i + 2 * j < g.N) o[16 * i + 2 * j] = (uint16_t)v[j];
+          if (n + 16 * i + 2 * j + 1 < g.N) o[16 * i + 2 * j + 1] = (uint16_t)(v[j] >> 16);
+        }
+      }
+    }
+  }
+}
+
+template <bool GROUPED>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const GemmArgs g,
+                int stages, int max_row_tiles, int vec) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + 2 * kScaleSlots];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int warp_sums[kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = (int)cluster_rank();  // 0: the pair's leader
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* const mem = smem_raw + (base - raw);
+  float* const scale_mem = reinterpret_cast<float*>(mem + stages * kStageBytes);  // [slot][weight block][row]
+  int* const table = reinterpret_cast<int*>(mem + stages * kStageBytes + kScaleBytes);
+  auto full = [&](int i) { return smem_u32(&bars[i]); };  // (the leader's: both CTAs' bytes)
+  auto empty = [&](int i) { return smem_u32(&bars[kMaxStages + i]); };
+  auto tfull = [&](int i) { return smem_u32(&bars[2 * kMaxStages + i]); };
+  auto tempty = [&](int i) { return smem_u32(&bars[2 * kMaxStages + kSlots + i]); };  // (the leader's)
+  auto sfull = [&](int i) { return smem_u32(&bars[2 * kMaxStages + 2 * kSlots + i]); };
+  auto sempty = [&](int i) { return smem_u32(&bars[2 * kMaxStages + 2 * kSlots + kScaleSlots + i]); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(tfull(i), 1);
+      mbar_init(tempty(i), 2 * kEpiWarps);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(sfull(i), 1);
+      mbar_init(sempty(i), kEpiWarps);
+    }
+    mbar_fence_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_a)) : "memory");
+  }
+  if (warp == kEpiWarps + 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(kSlots * kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tcgen05_before_sync();
+  cluster_sync();  // the peer's barriers are initialised before anything may arrive on them
+  tcgen05_after_sync();
+  const uint32_t tmem = tmem_slot;
+  grid_wait();
+  grid_launch_dependents();
+  const int nt = (g.nbn + 1) / 2;
+  int tiles;
+  if constexpr (GROUPED) {
+    tile_table(g, kRows, table, warp_sums);
+    tiles = min(table[g.E], max_row_tiles) * nt;
+  } else {
+    tiles = ((g.M - 1) / kRows + 1) * nt;
+  }
+  const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (warp == kEpiWarps) {  // TMA producer
+    int it = 0;
+    bool ok = true;
+    for (int t = t0; t < tiles && ok; t += step) {
+      const Tile ti = tile_at<GROUPED>(g, table, t, half);
+      int r[4] = {0, 0, 0, 0};  // rows 4 lane .. 4 lane + 3 (row 0 for those past the end)
+      if constexpr (GROUPED) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = 4 * lane + i;
+          long long in = -1, out;
+          if (c < ti.cnt) pair_rows(g, ti.pos + c, &in, &out);
+          r[i] = in < 0 ? 0 : (int)in;
+        }
+      }
+      const int wrow = ti.e * g.N + ti.n0 + half * 128;
+      for (int kb = 0; kb < g.nbk; ++kb, ++it) {
+        const int st = it % stages;
+        ok = __all_sync(kFullMask, mbar_wait(empty(st), ((uint32_t)(it / stages) & 1u) ^ 1u, g.err));
+        if (!ok) break;
+        const uint32_t dst = base + st * kStageBytes, bar = map_rank(full(st), 0);
+        if (lane == 0) {
+          if (half == 0) mbar_expect_tx(full(st), 2 * kStageBytes);
+          tma_load_2d_pair(dst + kHalf, &tm_w, kb * FP8_BLOCK, wrow, bar);
+          if (!GROUPED) tma_load_2d_pair(dst, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
+        }
+        __syncwarp();
+        if (GROUPED) tma_gather4_pair(dst + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
+      }
+    }
+    // the pair's copies still in flight land before either CTA may exit
+    if (half == 0)
+      for (int i = it > stages ? it - stages : 0; i < it; ++i) mbar_wait(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
+  } else if (warp == kEpiWarps + 1) {  // MMA issuer
+    if (lane == 0 && half == 0) {
+      constexpr uint32_t idesc = instr_desc_e4m3(kCols, kRows);
+      int it = 0;
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += step) {
+        for (int kb = 0; kb < g.nbk; ++kb, ++it) {
+          const int st = it % stages, sl = it % kSlots;
+          ok = mbar_wait(tempty(sl), ((uint32_t)(it / kSlots) & 1u) ^ 1u, g.err) &&
+               mbar_wait(full(st), (uint32_t)(it / stages) & 1u, g.err);
+          if (!ok) break;
+          tcgen05_after_sync();
+          const uint32_t aa = base + st * kStageBytes, wa = aa + kHalf;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_e4m3_pair(tmem + sl * kCols, sw128_desc(aa + 32u * k), sw128_desc(wa + 32u * k), idesc, k > 0 ? 1u : 0u);
+          mma_commit_pair(empty(st), (uint16_t)3);
+          mma_commit_pair(tfull(sl), (uint16_t)3);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kEpiWarps + 2) {  // scales
+    int it = 0;
+    bool ok = true;
+    for (int t = t0; t < tiles && ok; t += step) {
+      const Tile ti = tile_at<GROUPED>(g, table, t, half);
+      const float* sap[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = lane + 32 * i;
+        long long in = -1, out;
+        if (c < ti.cnt) {
+          if constexpr (GROUPED)
+            pair_rows(g, ti.pos + c, &in, &out);
+          else
+            in = ti.pos + c;
+        }
+        sap[i] = in < 0 ? nullptr : g.sa + in * g.nbk;
+      }
+      const int wb = ti.n0 / FP8_BLOCK;
+      const float* sw0 = g.sw + ((long long)ti.e * g.nbn + wb) * g.nbk;
+      const float* sw1 = wb + 1 < g.nbn ? sw0 + g.nbk : sw0;
+      float s[4], b0 = 0.f, b1 = 0.f;
+      auto fetch = [&](int kb) {
+        b0 = __ldg(sw0 + kb);
+        b1 = __ldg(sw1 + kb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = sap[i] ? __ldg(sap[i] + kb) : 0.f;
+      };
+      fetch(0);
+      for (int kb = 0; kb < g.nbk; ++kb, ++it) {
+        const int sl = it % kScaleSlots;
+        ok = __all_sync(kFullMask, mbar_wait(sempty(sl), ((uint32_t)(it / kScaleSlots) & 1u) ^ 1u, g.err));
+        if (!ok) break;
+        float* d = scale_mem + sl * 256 + lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d[32 * i] = __fmul_rn(s[i], b0);
+          d[128 + 32 * i] = __fmul_rn(s[i], b1);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull(sl));
+        if (kb + 1 < g.nbk) fetch(kb + 1);
+      }
+    }
+  } else {  // epilogue
+    const int q = warp & 3, cg = warp >> 2, row = q * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + cg * 64;
+    uint32_t tempty_lead[kSlots];
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) tempty_lead[i] = map_rank(tempty(i), 0);
+    int it = 0;
+    bool ok = true;
+    for (int t = t0; t < tiles && ok; t += step) {
+      uint64_t acc[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc[i] = 0;
+      for (int kb = 0; kb < g.nbk; ++kb, ++it) {
+        const int sl = it % kSlots, ss = it % kScaleSlots;
+        ok = __all_sync(kFullMask, mbar_wait(sfull(ss), (uint32_t)(it / kScaleSlots) & 1u, g.err) &&
+                                       mbar_wait(tfull(sl), (uint32_t)(it / kSlots) & 1u, g.err));
+        if (!ok) break;
+        tcgen05_after_sync();
+        const float sv = scale_mem[ss * 256 + (cg >> 1) * 128 + row];
+        const uint64_t s2 = pack2(__float_as_uint(sv), __float_as_uint(sv));
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint32_t v[16];
+          tmem_ld16(tl + sl * kCols + 16 * p, v);
+          tmem_wait_ld();
+          tmem_loaded(v);
+          if (p == 3) {  // the slots are read
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_cluster(tempty_lead[sl]);
+              mbar_arrive(sempty(ss));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[8 * p + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), s2, acc[8 * p + i]);
+        }
+      }
+      if (!ok) break;
+      const Tile ti = tile_at<GROUPED>(g, table, t, half);
+      if (row < ti.cnt) {
+        long long in, out = ti.pos + row;
+        if constexpr (GROUPED) pair_rows(g, ti.pos + row, &in, &out);
+        const int n = ti.n0 + cg * 64;
+        if (out >= 0 && n < g.N) store_row(g, out, n, acc, vec && n + 64 <= g.N);
+      }
+    }
+  }
+  tcgen05_before_sync();
+  __syncwarp();
+  cluster_sync();  // neither CTA leaves while the other may still touch its shared memory
+  if (warp == kEpiWarps + 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kSlots * kCols));
+}
+
+template <bool GROUPED>
+int launch(const GemmArgs& g, int sm_count, cudaStream_t stream) {
+  CUtensorMap tm_w, tm_a;
+  if (!make_code_map(&tm_w, g.w, (long long)g.E * g.N, g.K, 128)) return MOE_ERR_CUDA;
+  if (!make_code_map(&tm_a, g.a, g.a_rows, g.K, GROUPED ? 1 : 128)) return MOE_ERR_CUDA;
+  auto kern = wide_kernel<GROUPED>;
+  const long long rows = GROUPED ? (long long)g.M / kRows + (g.E < g.M ? g.E : g.M) : ((long long)g.M - 1) / kRows + 1;
+  const long long tiles = rows * ((g.nbn + 1) / 2);
+  if (tiles >= (1LL << 31) - (1 << 16) || rows >= kMaxRowTiles) return MOE_ERR_CAPACITY;
+  const size_t extra = 1024 + kScaleBytes + (GROUPED ? (g.E + 1) * 4 : 0);
+  int stages = (int)((kMaxSmem - kStaticSmem - extra) / kStageBytes);
+  if (stages > kMaxStages) stages = kMaxStages;
+  // All the shared memory a CTA may have: the pair holds both SMs' TMEM whole, so nothing
+  // that allocates TMEM may share them.
+  const size_t smem = kMaxSmem - kStaticSmem;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+      prefer_max_shared(reinterpret_cast<const void*>(kern)) != MOE_OK)
+    return MOE_ERR_CUDA;
+  const size_t esize = g.f32 ? 4 : 2;
+  const int vec = aligned(g.out, 32) && ((size_t)g.N * esize) % 32 == 0;
+  const int pairs = sm_count / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)(tiles < pairs ? tiles : pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_a, g, stages, (int)rows, vec) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_wide(const GemmArgs& g, int sm_count, cudaStream_t stream) {
+  return g.offsets ? launch<true>(g, sm_count, stream) : launch<false>(g, sm_count, stream);
+}
+
+}  // namespace fp8_impl
+}  // namespace moe
