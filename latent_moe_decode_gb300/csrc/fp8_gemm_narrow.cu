@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kThreads)
   const int kb0 = (int)((long long)rank * g.nbk / S), kb1 = (int)((long long)(rank + 1) * g.nbk / S);
 
   if (warp == 4) {  // TMA producer
-    int it = 0;     // stages issued
+    Ring st;
+    int issued = 0;
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       const Tile ti = tile_at<BN, GROUPED>(g, table, t);
@@ -137,42 +138,47 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
       const int wrow = ti.e * g.N + ti.n0;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int st = it % stages;
-        ok = __all_sync(kFullMask, mbar_wait(empty(st), ((uint32_t)(it / stages) & 1u) ^ 1u, g.err));
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = __all_sync(kFullMask, mbar_wait(empty(st.slot), st.lap ^ 1u, g.err));
         if (!ok) break;
-        const uint32_t dst = base + st * C::kStageBytes;
-        if (lane == 0) {
-          mbar_expect_tx(full(st), C::kStageBytes);
-          tma_load_2d(dst, &tm_w, kb * FP8_BLOCK, wrow, full(st));
-          if (!GROUPED) tma_load_2d(dst + kWBytes, &tm_a, kb * FP8_BLOCK, ti.pos, full(st));
+        const uint32_t dst = base + st.slot * C::kStageBytes, bar = full(st.slot);
+        if (elect_one()) {
+          mbar_expect_tx(bar, C::kStageBytes);
+          tma_load_2d(dst, &tm_w, kb * FP8_BLOCK, wrow, bar);
+          if (!GROUPED) tma_load_2d(dst + kWBytes, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
         }
         __syncwarp();
         if (GROUPED && lane < BN / 4)
-          tma_gather4(dst + kWBytes + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], full(st));
+          tma_gather4(dst + kWBytes + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
+        st.next(stages);
+        ++issued;
       }
     }
     // the copies still in flight land before the CTA may exit
-    for (int i = it > stages ? it - stages : 0; i < it; ++i) mbar_wait(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
+    for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+      mbar_wait(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
   } else if (warp == 5) {  // MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = instr_desc_e4m3(BN, 128);
-      int it = 0;
-      bool ok = true;
-      for (int t = t0; t < tiles && ok; t += step) {
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int st = it % stages, sl = it % C::kSlots;
-          ok = mbar_wait(tempty(sl), ((uint32_t)(it / C::kSlots) & 1u) ^ 1u, g.err) &&
-               mbar_wait(full(st), (uint32_t)(it / stages) & 1u, g.err);
-          if (!ok) break;
-          tcgen05_after_sync();
-          const uint32_t wa = base + st * C::kStageBytes, aa = wa + kWBytes;
+    // (the whole warp walks the loop, so that descriptors stay in uniform registers)
+    constexpr uint32_t idesc = instr_desc_e4m3(BN, 128);
+    const uint64_t weights0 = sw128_desc(base), rows0 = sw128_desc(base + kWBytes);
+    Ring st, sl;
+    bool ok = true;
+    for (int t = t0; t < tiles && ok; t += step) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = __all_sync(kFullMask, mbar_wait(tempty(sl.slot), sl.lap ^ 1u, g.err) && mbar_wait(full(st.slot), st.lap, g.err));
+        if (!ok) break;
+        tcgen05_after_sync();
+        const uint64_t at = (uint64_t)(st.slot * (C::kStageBytes >> 4));
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_e4m3(tmem + sl * BN, sw128_desc(wa + 32u * k), sw128_desc(aa + 32u * k), idesc, k > 0 ? 1u : 0u);
-          mma_commit(empty(st));
-          mma_commit(tfull(sl));
+            mma_e4m3(tmem + sl.slot * BN, weights0 + at + 2 * k, rows0 + at + 2 * k, idesc, k > 0 ? 1u : 0u);
+          mma_commit(empty(st.slot));
+          mma_commit(tfull(sl.slot));
         }
+        __syncwarp();
+        st.next(stages);
+        sl.next(C::kSlots);
       }
     }
     __syncwarp();
@@ -181,7 +187,8 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int P = BN < 32 ? BN : 32;  // columns per TMEM load
     float* const sc = scale_mem + warp * 2 * BN;
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
-    int it = 0;
+    Ring sl;
+    int parity = 0;  // of the warp's scale buffers
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       const Tile ti = tile_at<BN, GROUPED>(g, table, t);
@@ -211,30 +218,29 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = 0; i < CL; ++i) s[i] = sap[i] ? __ldg(sap[i] + kb) : 0.f;
       };
       fetch(kb0);
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        float* const buf = sc + (it & 1) * BN;  // (the other parity may still be read by slower lanes)
+      for (int kb = kb0; kb < kb1; ++kb) {
+        float* const buf = sc + parity * BN;  // (the other parity may still be read by slower lanes)
 #pragma unroll
         for (int i = 0; i < CL; ++i)
           if (lane + 32 * i < BN) buf[lane + 32 * i] = __fmul_rn(s[i], b);
         if (kb + 1 < kb1) fetch(kb + 1);
         __syncwarp();
-        const int sl = it % C::kSlots;
-        ok = __all_sync(kFullMask, mbar_wait(tfull(sl), (uint32_t)(it / C::kSlots) & 1u, g.err));
+        ok = __all_sync(kFullMask, mbar_wait(tfull(sl.slot), sl.lap, g.err));
         if (!ok) break;
         tcgen05_after_sync();
 #pragma unroll
         for (int p = 0; p < BN / P; ++p) {
           uint32_t v[P];
           if constexpr (P == 16)
-            tmem_ld16(tl + sl * BN, v);
+            tmem_ld16(tl + sl.slot * BN, v);
           else
-            tmem_ld32(tl + sl * BN + p * P, v);
+            tmem_ld32(tl + sl.slot * BN + p * P, v);
           tmem_wait_ld();
           tmem_loaded(v);
           if (p == BN / P - 1) {  // the slot is read
             tcgen05_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty(sl));
+            if (lane == 0) mbar_arrive(tempty(sl.slot));
           }
 #pragma unroll
           for (int i = 0; i < P / 4; ++i) {
@@ -244,6 +250,8 @@ __global__ void __launch_bounds__(kThreads)
             a[1] = fma2(pack2(v[4 * i + 2], v[4 * i + 3]), f.y, a[1]);
           }
         }
+        parity ^= 1;
+        sl.next(C::kSlots);
       }
       if (!ok) break;
       const int n = ti.n0 + threadIdx.x;  // this thread's weight row

@@ -9,11 +9,11 @@
 // number for 128 columns:
 //   - warps 0-15: epilogue. Warp w reads lanes 32 (w % 4).. and columns 64 (w / 4)..,
 //     and folds each block's sums, times sa sw, into 64 FP32 registers a thread;
-//   - warp 16: TMA producer (rows of an expert's list by gather4, four at a time);
-//   - warp 17: MMA issuer (in the pair's even CTA, for both);
-//   - warp 18: scales. It walks the rows' scales ahead of the epilogue and leaves the
-//     products sa sw of a block, for both weight blocks of the tile, in a ring in shared
-//     memory, so that the row-major scales are fetched once per CTA and not per warp.
+//   - warp 16: TMA producer (rows of an expert's list by gather4, four at a time), which
+//     also walks the rows' scales and leaves the products sa sw of a block, for both
+//     weight blocks of the tile, in a ring in shared memory: the row-major scales are
+//     fetched once per CTA and not per warp, ahead of the epilogue;
+//   - warp 17: MMA issuer (in the pair's even CTA, for both).
 // A persistent grid of pairs walks the tiles, row tiles of the same weights side by side.
 #include "fp8_gemm.cuh"
 
@@ -22,13 +22,16 @@ namespace fp8_impl {
 namespace {
 
 constexpr int kEpiWarps = 16;
-constexpr int kThreads = 32 * (kEpiWarps + 3);
+constexpr int kThreads = 32 * (kEpiWarps + 2);
 constexpr int kRows = 256, kCols = 256;       // a pair's tile
 constexpr int kHalf = 128 * FP8_BLOCK;        // bytes of one CTA's rows, or weights, of a stage
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kMaxStages = 6;
 constexpr int kSlots = 2;                     // TMEM accumulators: all 512 columns
-constexpr int kScaleSlots = 4;
+// Scale slots. A slot needs no barrier of its own to be free: when the producer reaches
+// block b + stages + kSlots it has seen the MMA of block b + kSlots complete, which was
+// issued once the epilogue had read block b's sums, after its scales.
+constexpr int kScaleSlots = kMaxStages + kSlots;
 constexpr int kScaleBytes = kScaleSlots * 2 * 128 * 4;
 
 struct Tile {
@@ -71,9 +74,10 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Arrive on a barrier of the cluster (a shared::cluster address).
+// Arrive on a barrier of the cluster (a shared::cluster address). Relaxed: what it reports is a
+// TMEM read, ordered by the tcgen05 fence; a release at cluster scope costs a memory barrier.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const GemmArgs g,
                 int stages, int max_row_tiles, int vec) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + 2 * kScaleSlots];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + kScaleSlots];
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sums[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -147,7 +151,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   auto tfull = [&](int i) { return smem_u32(&bars[2 * kMaxStages + i]); };
   auto tempty = [&](int i) { return smem_u32(&bars[2 * kMaxStages + kSlots + i]); };  // (the leader's)
   auto sfull = [&](int i) { return smem_u32(&bars[2 * kMaxStages + 2 * kSlots + i]); };
-  auto sempty = [&](int i) { return smem_u32(&bars[2 * kMaxStages + 2 * kSlots + kScaleSlots + i]); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
@@ -158,10 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(tfull(i), 1);
       mbar_init(tempty(i), 2 * kEpiWarps);
     }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(sfull(i), 1);
-      mbar_init(sempty(i), kEpiWarps);
-    }
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(sfull(i), 1);
     mbar_fence_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_a)) : "memory");
@@ -187,70 +187,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   }
   const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-  if (warp == kEpiWarps) {  // TMA producer
-    int it = 0;
+  if (warp == kEpiWarps) {  // TMA producer and scales
+    Ring st, sc;
+    int issued = 0;
+    const uint32_t ring = stages + kSlots, lead = map_rank(full(0), 0);
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       const Tile ti = tile_at<GROUPED>(g, table, t, half);
       int r[4] = {0, 0, 0, 0};  // rows 4 lane .. 4 lane + 3 (row 0 for those past the end)
-      if constexpr (GROUPED) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 4 * lane + i;
-          long long in = -1, out;
-          if (c < ti.cnt) pair_rows(g, ti.pos + c, &in, &out);
-          r[i] = in < 0 ? 0 : (int)in;
-        }
-      }
-      const int wrow = ti.e * g.N + ti.n0 + half * 128;
-      for (int kb = 0; kb < g.nbk; ++kb, ++it) {
-        const int st = it % stages;
-        ok = __all_sync(kFullMask, mbar_wait(empty(st), ((uint32_t)(it / stages) & 1u) ^ 1u, g.err));
-        if (!ok) break;
-        const uint32_t dst = base + st * kStageBytes, bar = map_rank(full(st), 0);
-        if (lane == 0) {
-          if (half == 0) mbar_expect_tx(full(st), 2 * kStageBytes);
-          tma_load_2d_pair(dst + kHalf, &tm_w, kb * FP8_BLOCK, wrow, bar);
-          if (!GROUPED) tma_load_2d_pair(dst, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
-        }
-        __syncwarp();
-        if (GROUPED) tma_gather4_pair(dst + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
-      }
-    }
-    // the pair's copies still in flight land before either CTA may exit
-    if (half == 0)
-      for (int i = it > stages ? it - stages : 0; i < it; ++i) mbar_wait(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
-  } else if (warp == kEpiWarps + 1) {  // MMA issuer
-    if (lane == 0 && half == 0) {
-      constexpr uint32_t idesc = instr_desc_e4m3(kCols, kRows);
-      int it = 0;
-      bool ok = true;
-      for (int t = t0; t < tiles && ok; t += step) {
-        for (int kb = 0; kb < g.nbk; ++kb, ++it) {
-          const int st = it % stages, sl = it % kSlots;
-          ok = mbar_wait(tempty(sl), ((uint32_t)(it / kSlots) & 1u) ^ 1u, g.err) &&
-               mbar_wait(full(st), (uint32_t)(it / stages) & 1u, g.err);
-          if (!ok) break;
-          tcgen05_after_sync();
-          const uint32_t aa = base + st * kStageBytes, wa = aa + kHalf;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_e4m3_pair(tmem + sl * kCols, sw128_desc(aa + 32u * k), sw128_desc(wa + 32u * k), idesc, k > 0 ? 1u : 0u);
-          mma_commit_pair(empty(st), (uint16_t)3);
-          mma_commit_pair(tfull(sl), (uint16_t)3);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == kEpiWarps + 2) {  // scales
-    int it = 0;
-    bool ok = true;
-    for (int t = t0; t < tiles && ok; t += step) {
-      const Tile ti = tile_at<GROUPED>(g, table, t, half);
-      const float* sap[4];
+      const float* sap[4];      // scales of the same rows
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int c = lane + 32 * i;
+        const int c = 4 * lane + i;
         long long in = -1, out;
         if (c < ti.cnt) {
           if constexpr (GROUPED)
@@ -258,9 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           else
             in = ti.pos + c;
         }
+        if (GROUPED) r[i] = in < 0 ? 0 : (int)in;
         sap[i] = in < 0 ? nullptr : g.sa + in * g.nbk;
       }
-      const int wb = ti.n0 / FP8_BLOCK;
+      const int wrow = ti.e * g.N + ti.n0 + half * 128, wb = ti.n0 / FP8_BLOCK;
       const float* sw0 = g.sw + ((long long)ti.e * g.nbn + wb) * g.nbk;
       const float* sw1 = wb + 1 < g.nbn ? sw0 + g.nbk : sw0;
       float s[4], b0 = 0.f, b1 = 0.f;
@@ -271,58 +220,94 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int i = 0; i < 4; ++i) s[i] = sap[i] ? __ldg(sap[i] + kb) : 0.f;
       };
       fetch(0);
-      for (int kb = 0; kb < g.nbk; ++kb, ++it) {
-        const int sl = it % kScaleSlots;
-        ok = __all_sync(kFullMask, mbar_wait(sempty(sl), ((uint32_t)(it / kScaleSlots) & 1u) ^ 1u, g.err));
+      for (int kb = 0; kb < g.nbk; ++kb) {
+        ok = __all_sync(kFullMask, mbar_wait(empty(st.slot), st.lap ^ 1u, g.err));
         if (!ok) break;
-        float* d = scale_mem + sl * 256 + lane;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          d[32 * i] = __fmul_rn(s[i], b0);
-          d[128 + 32 * i] = __fmul_rn(s[i], b1);
+        const uint32_t dst = base + st.slot * kStageBytes, bar = lead + 8 * st.slot;
+        if (elect_one()) {
+          if (half == 0) mbar_expect_tx(full(st.slot), 2 * kStageBytes);
+          tma_load_2d_pair(dst + kHalf, &tm_w, kb * FP8_BLOCK, wrow, bar);
+          if (!GROUPED) tma_load_2d_pair(dst, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(sfull(sl));
+        if (GROUPED) tma_gather4_pair(dst + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
+        float4* d = reinterpret_cast<float4*>(scale_mem + sc.slot * 256) + lane;
+        d[0] = make_float4(__fmul_rn(s[0], b0), __fmul_rn(s[1], b0), __fmul_rn(s[2], b0), __fmul_rn(s[3], b0));
+        d[32] = make_float4(__fmul_rn(s[0], b1), __fmul_rn(s[1], b1), __fmul_rn(s[2], b1), __fmul_rn(s[3], b1));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull(sc.slot));
         if (kb + 1 < g.nbk) fetch(kb + 1);
+        st.next(stages);
+        sc.next(ring);
+        ++issued;
       }
     }
+    // the pair's copies still in flight land before either CTA may exit
+    if (half == 0)
+      for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+        mbar_wait(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
+  } else if (warp == kEpiWarps + 1) {  // MMA issuer
+    // (the whole warp walks the loop, so that descriptors stay in uniform registers)
+    if (half == 0) {
+      constexpr uint32_t idesc = instr_desc_e4m3(kCols, kRows);
+      const uint64_t rows0 = sw128_desc(base), weights0 = sw128_desc(base + kHalf);
+      Ring st, sl;
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += step) {
+        for (int kb = 0; kb < g.nbk; ++kb) {
+          ok = __all_sync(kFullMask, mbar_wait(tempty(sl.slot), sl.lap ^ 1u, g.err) && mbar_wait(full(st.slot), st.lap, g.err));
+          if (!ok) break;
+          tcgen05_after_sync();
+          const uint64_t at = (uint64_t)(st.slot * (kStageBytes >> 4));
+          const uint32_t d = tmem + sl.slot * kCols;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_e4m3_pair(d, rows0 + at + 2 * k, weights0 + at + 2 * k, idesc, k > 0 ? 1u : 0u);
+            mma_commit_pair(empty(st.slot), (uint16_t)3);
+            mma_commit_pair(tfull(sl.slot), (uint16_t)3);
+          }
+          __syncwarp();
+          st.next(stages);
+          sl.next(kSlots);
+        }
+      }
+    }
+    __syncwarp();
   } else {  // epilogue
     const int q = warp & 3, cg = warp >> 2, row = q * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + cg * 64;
-    uint32_t tempty_lead[kSlots];
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) tempty_lead[i] = map_rank(tempty(i), 0);
-    int it = 0;
+    const float* const sc = scale_mem + (cg >> 1) * 128 + row;
+    const uint32_t lead = map_rank(tempty(0), 0);  // the leader's tempty(0); tempty(1) follows it
+    const uint32_t ring = stages + kSlots;
+    Ring sl, ss;  // TMEM and scale slots
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       uint64_t acc[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[i] = 0;
-      for (int kb = 0; kb < g.nbk; ++kb, ++it) {
-        const int sl = it % kSlots, ss = it % kScaleSlots;
-        ok = __all_sync(kFullMask, mbar_wait(sfull(ss), (uint32_t)(it / kScaleSlots) & 1u, g.err) &&
-                                       mbar_wait(tfull(sl), (uint32_t)(it / kSlots) & 1u, g.err));
+      for (int kb = 0; kb < g.nbk; ++kb) {
+        ok = mbar_wait(sfull(ss.slot), ss.lap, g.err);
+        const float sv = sc[ss.slot * 256];
+        ok = __all_sync(kFullMask, ok && mbar_wait(tfull(sl.slot), sl.lap, g.err));
         if (!ok) break;
         tcgen05_after_sync();
-        const float sv = scale_mem[ss * 256 + (cg >> 1) * 128 + row];
         const uint64_t s2 = pack2(__float_as_uint(sv), __float_as_uint(sv));
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           uint32_t v[16];
-          tmem_ld16(tl + sl * kCols + 16 * p, v);
+          tmem_ld16(tl + sl.slot * kCols + 16 * p, v);
           tmem_wait_ld();
           tmem_loaded(v);
           if (p == 3) {  // the slots are read
             tcgen05_before_sync();
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_cluster(tempty_lead[sl]);
-              mbar_arrive(sempty(ss));
-            }
+            if (lane == 0) mbar_arrive_cluster(lead + 8 * sl.slot);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[8 * p + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), s2, acc[8 * p + i]);
         }
+        sl.next(kSlots);
+        ss.next(ring);
       }
       if (!ok) break;
       const Tile ti = tile_at<GROUPED>(g, table, t, half);
@@ -332,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int n = ti.n0 + cg * 64;
         if (out >= 0 && n < g.N) store_row(g, out, n, acc, vec && n + 64 <= g.N);
       }
+      __syncwarp();
     }
   }
   tcgen05_before_sync();

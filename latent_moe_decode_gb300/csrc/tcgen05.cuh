@@ -109,6 +109,22 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&v)[N]) {
 __device__ __forceinline__ void tcgen05_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tcgen05_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// One lane of a converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
+// A position in a ring of `n` slots and the parity of its lap: the issue loops step it
+// (a division by a run-time count would cost more than their waits).
+struct Ring {
+  uint32_t slot = 0, lap = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++slot == n) slot = 0, lap ^= 1u;
+  }
+};
+
 // The driver's tensor-map encoder (nullptr when the driver lacks it).
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
