@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads)
       }
       const int wrow = ti.e * g.N + ti.n0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = __all_sync(kFullMask, mbar_wait(empty(st.slot), st.lap ^ 1u, g.err));
+        ok = __all_sync(kFullMask, mbar_wait_asleep(empty(st.slot), st.lap ^ 1u, g.err));
         if (!ok) break;
         const uint32_t dst = base + st.slot * C::kStageBytes, bar = full(st.slot);
         if (elect_one()) {
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     // the copies still in flight land before the CTA may exit
     for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-      mbar_wait(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
+      mbar_wait_asleep(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
   } else if (warp == 5) {  // MMA issuer
     // (the whole warp walks the loop, so that descriptors stay in uniform registers)
     constexpr uint32_t idesc = instr_desc_e4m3(BN, 128);
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads)
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = __all_sync(kFullMask, mbar_wait(tempty(sl.slot), sl.lap ^ 1u, g.err) && mbar_wait(full(st.slot), st.lap, g.err));
+        ok = __all_sync(kFullMask, mbar_wait_asleep(tempty(sl.slot), sl.lap ^ 1u, g.err) && mbar_wait_asleep(full(st.slot), st.lap, g.err));
         if (!ok) break;
         tcgen05_after_sync();
         const uint64_t at = (uint64_t)(st.slot * (C::kStageBytes >> 4));
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads)
           if (lane + 32 * i < BN) buf[lane + 32 * i] = __fmul_rn(s[i], b);
         if (kb + 1 < kb1) fetch(kb + 1);
         __syncwarp();
-        ok = __all_sync(kFullMask, mbar_wait(tfull(sl.slot), sl.lap, g.err));
+        ok = __all_sync(kFullMask, mbar_wait_asleep(tfull(sl.slot), sl.lap, g.err));
         if (!ok) break;
         tcgen05_after_sync();
 #pragma unroll

@@ -1,19 +1,21 @@
 // Block-128 E4M3 product for many rows per weight tile (prompts, experts with hundreds of
 // rows): rows on the tensor core's lanes, weights on its columns, two SMs per tile.
 //
-// Bound by the tensor cores. A pair of CTAs runs one M = 256, N = 256 MMA (cta_group::2)
-// over 256 rows of a (128 lanes of each CTA) and 256 weight rows (128 staged by each), so
-// an SM stages 32 KB per block of 128 columns for 512 cycles of multiplication: half of
-// what two single CTAs would draw from L2 for the same work. A block's sum stays in one
-// of two TMEM slots of 256 columns; with the rows on the lanes a thread's scale is one
-// number for 128 columns:
-//   - warps 0-15: epilogue. Warp w reads lanes 32 (w % 4).. and columns 64 (w / 4)..,
-//     and folds each block's sums, times sa sw, into 64 FP32 registers a thread;
-//   - warp 16: TMA producer (rows of an expert's list by gather4, four at a time), which
-//     also walks the rows' scales and leaves the products sa sw of a block, for both
-//     weight blocks of the tile, in a ring in shared memory: the row-major scales are
-//     fetched once per CTA and not per warp, ahead of the epilogue;
-//   - warp 17: MMA issuer (in the pair's even CTA, for both).
+// Bound by the tensor cores. A pair of CTAs (cta_group::2, M = 256) works on 256 rows of
+// a (128 lanes of each CTA) and 256 weight rows (128 staged by each), so an SM stages 32
+// KB per block of 128 columns for 512 cycles of multiplication: half of what two single
+// CTAs would draw from L2 for the same work. The columns are multiplied in two halves of
+// 128, each with two TMEM slots of its own: one half's sums are read while the other
+// half multiplies. With the rows on the lanes a thread's scale is one number for a half:
+//   - warps 0-15: epilogue. Warp w reads lanes 32 (w % 4).. and columns 64 (w / 4).. and
+//     folds each block's sums, times its scale, into 64 FP32 registers a thread;
+//   - warp 16: TMA producer (rows of an expert's list by gather4, four at a time);
+//   - warps 17 and 18: MMA issuers, one for each half of the columns (in the pair's even
+//     CTA, for both): among the epilogue warps one warp's issue loop took longer than the
+//     multiplication it issues;
+//   - warp 19: scales. It walks the rows' scales ahead of the epilogue and leaves the
+//     products sa sw of a block, for both halves, in a ring in shared memory, so that
+//     the row-major scales are fetched once per CTA and not per warp.
 // A persistent grid of pairs walks the tiles, row tiles of the same weights side by side.
 #include "fp8_gemm.cuh"
 
@@ -22,16 +24,13 @@ namespace fp8_impl {
 namespace {
 
 constexpr int kEpiWarps = 16;
-constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kThreads = 32 * (kEpiWarps + 4);
 constexpr int kRows = 256, kCols = 256;       // a pair's tile
 constexpr int kHalf = 128 * FP8_BLOCK;        // bytes of one CTA's rows, or weights, of a stage
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kMaxStages = 6;
-constexpr int kSlots = 2;                     // TMEM accumulators: all 512 columns
-// Scale slots. A slot needs no barrier of its own to be free: when the producer reaches
-// block b + stages + kSlots it has seen the MMA of block b + kSlots complete, which was
-// issued once the epilogue had read block b's sums, after its scales.
-constexpr int kScaleSlots = kMaxStages + kSlots;
+constexpr int kStages = 6;
+constexpr int kSlots = 2;                     // TMEM accumulators of each half of the columns: all 512 columns
+constexpr int kScaleSlots = 4;
 constexpr int kScaleBytes = kScaleSlots * 2 * 128 * 4;
 
 struct Tile {
@@ -88,18 +87,14 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {
 
 // 64 outputs of one row from column n on: whole 32-byte sectors a store where the rows
 // are so aligned and the columns all exist (vec), else one by one.
-__device__ __forceinline__ void store_row(const GemmArgs& g, long long row, int n, const uint64_t (&acc)[32], bool vec) {
+__device__ __forceinline__ void store_row(const GemmArgs& g, long long row, int n, const float (&acc)[64], bool vec) {
   if (g.f32) {
     float* o = static_cast<float*>(g.out) + row * g.N + n;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t v[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float lo, hi;
-        unpack2(acc[4 * i + j], &lo, &hi);
-        v[2 * j] = __float_as_uint(lo), v[2 * j + 1] = __float_as_uint(hi);
-      }
+      for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(acc[8 * i + j]);
       if (vec) {
         st32(o + 8 * i, v);
       } else {
@@ -114,11 +109,7 @@ __device__ __forceinline__ void store_row(const GemmArgs& g, long long row, int 
     for (int i = 0; i < 4; ++i) {
       uint32_t v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float lo, hi;
-        unpack2(acc[8 * i + j], &lo, &hi);
-        v[j] = pack_bf16x2(lo, hi);
-      }
+      for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(acc[16 * i + 2 * j], acc[16 * i + 2 * j + 1]);
       if (vec) {
         st32(o + 16 * i, v);
       } else {
@@ -135,33 +126,38 @@ __device__ __forceinline__ void store_row(const GemmArgs& g, long long row, int 
 template <bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const GemmArgs g,
-                int stages, int max_row_tiles, int vec) {
+                int max_row_tiles, int vec) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + kScaleSlots];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 4 * kSlots + 2 * kScaleSlots];
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sums[kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = (int)cluster_rank();  // 0: the pair's leader
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const mem = smem_raw + (base - raw);
-  float* const scale_mem = reinterpret_cast<float*>(mem + stages * kStageBytes);  // [slot][weight block][row]
-  int* const table = reinterpret_cast<int*>(mem + stages * kStageBytes + kScaleBytes);
+  float* const scale_mem = reinterpret_cast<float*>(mem + kStages * kStageBytes);  // [slot][weight block][row]
+  int* const table = reinterpret_cast<int*>(mem + kStages * kStageBytes + kScaleBytes);
   auto full = [&](int i) { return smem_u32(&bars[i]); };  // (the leader's: both CTAs' bytes)
-  auto empty = [&](int i) { return smem_u32(&bars[kMaxStages + i]); };
-  auto tfull = [&](int i) { return smem_u32(&bars[2 * kMaxStages + i]); };
-  auto tempty = [&](int i) { return smem_u32(&bars[2 * kMaxStages + kSlots + i]); };  // (the leader's)
-  auto sfull = [&](int i) { return smem_u32(&bars[2 * kMaxStages + 2 * kSlots + i]); };
+  auto empty = [&](int i) { return smem_u32(&bars[kStages + i]); };
+  // (slot, column half): the sums are there; they are read (the leader's: both CTAs' warps)
+  auto tfull = [&](int i, int h) { return smem_u32(&bars[2 * kStages + 2 * i + h]); };
+  auto tempty = [&](int i, int h) { return smem_u32(&bars[2 * kStages + 2 * kSlots + 2 * i + h]); };
+  auto sfull = [&](int i) { return smem_u32(&bars[2 * kStages + 4 * kSlots + i]); };
+  auto sempty = [&](int i) { return smem_u32(&bars[2 * kStages + 4 * kSlots + kScaleSlots + i]); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < stages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(full(i), 1);
-      mbar_init(empty(i), 1);
+      mbar_init(empty(i), 2);  // both issuers
     }
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(tfull(i), 1);
-      mbar_init(tempty(i), 2 * kEpiWarps);
+    for (int i = 0; i < 2 * kSlots; ++i) {
+      mbar_init(tfull(i >> 1, i & 1), 1);
+      mbar_init(tempty(i >> 1, i & 1), kEpiWarps);  // half the epilogue warps of each CTA
     }
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(sfull(i), 1);
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(sfull(i), 1);
+      mbar_init(sempty(i), kEpiWarps);
+    }
     mbar_fence_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_a)) : "memory");
@@ -187,15 +183,78 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   }
   const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-  if (warp == kEpiWarps) {  // TMA producer and scales
-    Ring st, sc;
+  if (warp == kEpiWarps) {  // TMA producer
+    Ring st;
     int issued = 0;
-    const uint32_t ring = stages + kSlots, lead = map_rank(full(0), 0);
+    const uint32_t lead = map_rank(full(0), 0);
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       const Tile ti = tile_at<GROUPED>(g, table, t, half);
       int r[4] = {0, 0, 0, 0};  // rows 4 lane .. 4 lane + 3 (row 0 for those past the end)
-      const float* sap[4];      // scales of the same rows
+      if constexpr (GROUPED) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = 4 * lane + i;
+          long long in = -1, out;
+          if (c < ti.cnt) pair_rows(g, ti.pos + c, &in, &out);
+          r[i] = in < 0 ? 0 : (int)in;
+        }
+      }
+      const int wrow = ti.e * g.N + ti.n0 + half * 64;
+      for (int kb = 0; kb < g.nbk; ++kb) {
+        ok = __all_sync(kFullMask, mbar_wait_asleep(empty(st.slot), st.lap ^ 1u, g.err));
+        if (!ok) break;
+        const uint32_t dst = base + st.slot * kStageBytes, bar = lead + 8 * st.slot;
+        if (elect_one()) {
+          if (half == 0) mbar_expect_tx(full(st.slot), 2 * kStageBytes);
+          tma_load_2d_pair(dst + kHalf, &tm_w, kb * FP8_BLOCK, wrow, bar);
+          tma_load_2d_pair(dst + kHalf + kHalf / 2, &tm_w, kb * FP8_BLOCK, wrow + 128, bar);
+          if (!GROUPED) tma_load_2d_pair(dst, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
+        }
+        __syncwarp();
+        if (GROUPED) tma_gather4_pair(dst + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
+        st.next(kStages);
+        ++issued;
+      }
+    }
+    // the pair's copies still in flight land before either CTA may exit
+    if (half == 0)
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+        mbar_wait_asleep(full(i % kStages), (uint32_t)(i / kStages) & 1u, g.err);
+  } else if (warp == kEpiWarps + 1 || warp == kEpiWarps + 2) {  // MMA issuers
+    // (the whole warp walks the loop, so that descriptors stay in uniform registers)
+    if (half == 0) {
+      constexpr uint32_t idesc = instr_desc_e4m3(kCols / 2, kRows);
+      const int h = warp - kEpiWarps - 1;
+      const uint64_t rows0 = sw128_desc(base), weights0 = sw128_desc(base + kHalf + h * (kHalf / 2));
+      Ring st, sl;
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += step) {
+        for (int kb = 0; kb < g.nbk; ++kb) {
+          ok = __all_sync(kFullMask, mbar_wait_asleep(tempty(sl.slot, h), sl.lap ^ 1u, g.err) && mbar_wait_asleep(full(st.slot), st.lap, g.err));
+          if (!ok) break;
+          tcgen05_after_sync();
+          const uint64_t at = (uint64_t)(st.slot * (kStageBytes >> 4));
+          const uint32_t d = tmem + sl.slot * kCols + h * (kCols / 2);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_e4m3_pair(d, rows0 + at + 2 * k, weights0 + at + 2 * k, idesc, k > 0 ? 1u : 0u);
+            mma_commit_pair(tfull(sl.slot, h), (uint16_t)3);
+            mma_commit_pair(empty(st.slot), (uint16_t)3);
+          }
+          __syncwarp();
+          st.next(kStages);
+          sl.next(kSlots);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kEpiWarps + 3) {  // scales
+    Ring sc;
+    bool ok = true;
+    for (int t = t0; t < tiles && ok; t += step) {
+      const Tile ti = tile_at<GROUPED>(g, table, t, half);
+      const float* sap[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = 4 * lane + i;
@@ -206,108 +265,69 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           else
             in = ti.pos + c;
         }
-        if (GROUPED) r[i] = in < 0 ? 0 : (int)in;
         sap[i] = in < 0 ? nullptr : g.sa + in * g.nbk;
       }
-      const int wrow = ti.e * g.N + ti.n0 + half * 128, wb = ti.n0 / FP8_BLOCK;
+      const int wb = ti.n0 / FP8_BLOCK;
       const float* sw0 = g.sw + ((long long)ti.e * g.nbn + wb) * g.nbk;
-      const float* sw1 = wb + 1 < g.nbn ? sw0 + g.nbk : sw0;
+      const int next = wb + 1 < g.nbn ? g.nbk : 0;  // to the second half's scales
       float s[4], b0 = 0.f, b1 = 0.f;
       auto fetch = [&](int kb) {
         b0 = __ldg(sw0 + kb);
-        b1 = __ldg(sw1 + kb);
+        b1 = __ldg(sw0 + next + kb);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = sap[i] ? __ldg(sap[i] + kb) : 0.f;
       };
       fetch(0);
       for (int kb = 0; kb < g.nbk; ++kb) {
-        ok = __all_sync(kFullMask, mbar_wait(empty(st.slot), st.lap ^ 1u, g.err));
+        ok = __all_sync(kFullMask, mbar_wait_asleep(sempty(sc.slot), sc.lap ^ 1u, g.err));
         if (!ok) break;
-        const uint32_t dst = base + st.slot * kStageBytes, bar = lead + 8 * st.slot;
-        if (elect_one()) {
-          if (half == 0) mbar_expect_tx(full(st.slot), 2 * kStageBytes);
-          tma_load_2d_pair(dst + kHalf, &tm_w, kb * FP8_BLOCK, wrow, bar);
-          if (!GROUPED) tma_load_2d_pair(dst, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
-        }
-        __syncwarp();
-        if (GROUPED) tma_gather4_pair(dst + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
         float4* d = reinterpret_cast<float4*>(scale_mem + sc.slot * 256) + lane;
         d[0] = make_float4(__fmul_rn(s[0], b0), __fmul_rn(s[1], b0), __fmul_rn(s[2], b0), __fmul_rn(s[3], b0));
         d[32] = make_float4(__fmul_rn(s[0], b1), __fmul_rn(s[1], b1), __fmul_rn(s[2], b1), __fmul_rn(s[3], b1));
         __syncwarp();
         if (lane == 0) mbar_arrive(sfull(sc.slot));
         if (kb + 1 < g.nbk) fetch(kb + 1);
-        st.next(stages);
-        sc.next(ring);
-        ++issued;
+        sc.next(kScaleSlots);
       }
     }
-    // the pair's copies still in flight land before either CTA may exit
-    if (half == 0)
-      for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-        mbar_wait(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
-  } else if (warp == kEpiWarps + 1) {  // MMA issuer
-    // (the whole warp walks the loop, so that descriptors stay in uniform registers)
-    if (half == 0) {
-      constexpr uint32_t idesc = instr_desc_e4m3(kCols, kRows);
-      const uint64_t rows0 = sw128_desc(base), weights0 = sw128_desc(base + kHalf);
-      Ring st, sl;
-      bool ok = true;
-      for (int t = t0; t < tiles && ok; t += step) {
-        for (int kb = 0; kb < g.nbk; ++kb) {
-          ok = __all_sync(kFullMask, mbar_wait(tempty(sl.slot), sl.lap ^ 1u, g.err) && mbar_wait(full(st.slot), st.lap, g.err));
-          if (!ok) break;
-          tcgen05_after_sync();
-          const uint64_t at = (uint64_t)(st.slot * (kStageBytes >> 4));
-          const uint32_t d = tmem + sl.slot * kCols;
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_e4m3_pair(d, rows0 + at + 2 * k, weights0 + at + 2 * k, idesc, k > 0 ? 1u : 0u);
-            mma_commit_pair(empty(st.slot), (uint16_t)3);
-            mma_commit_pair(tfull(sl.slot), (uint16_t)3);
-          }
-          __syncwarp();
-          st.next(stages);
-          sl.next(kSlots);
-        }
-      }
-    }
-    __syncwarp();
   } else {  // epilogue
-    const int q = warp & 3, cg = warp >> 2, row = q * 32 + lane;
+    const int q = warp & 3, cg = warp >> 2, h = cg >> 1, row = q * 32 + lane;  // half h of the columns
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + cg * 64;
-    const float* const sc = scale_mem + (cg >> 1) * 128 + row;
-    const uint32_t lead = map_rank(tempty(0), 0);  // the leader's tempty(0); tempty(1) follows it
-    const uint32_t ring = stages + kSlots;
+    const float* const sc = scale_mem + h * 128 + row;
+    const uint32_t lead = map_rank(tempty(0, h), 0);  // the leader's; the next slot's is 16 bytes on
     Ring sl, ss;  // TMEM and scale slots
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
-      uint64_t acc[32];
+      float acc[64];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[i] = 0;
+      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
       for (int kb = 0; kb < g.nbk; ++kb) {
-        ok = mbar_wait(sfull(ss.slot), ss.lap, g.err);
+        ok = mbar_wait_asleep(sfull(ss.slot), ss.lap, g.err);
         const float sv = sc[ss.slot * 256];
-        ok = __all_sync(kFullMask, ok && mbar_wait(tfull(sl.slot), sl.lap, g.err));
+        ok = __all_sync(kFullMask, ok && mbar_wait_asleep(tfull(sl.slot, h), sl.lap, g.err));
         if (!ok) break;
         tcgen05_after_sync();
-        const uint64_t s2 = pack2(__float_as_uint(sv), __float_as_uint(sv));
+        const uint32_t col = tl + sl.slot * kCols;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           uint32_t v[16];
-          tmem_ld16(tl + sl.slot * kCols + 16 * p, v);
+          tmem_ld16(col + 16 * p, v);
           tmem_wait_ld();
           tmem_loaded(v);
-          if (p == 3) {  // the slots are read
+          if (p == 3) {  // the slot is read
             tcgen05_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead + 8 * sl.slot);
+            if (lane == 0) {
+              mbar_arrive_cluster(lead + 16 * sl.slot);
+              mbar_arrive(sempty(ss.slot));
+            }
           }
+          // (FFMA and not the packed form, whose operand pairs cost two moves each here)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[8 * p + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), s2, acc[8 * p + i]);
+          for (int i = 0; i < 16; ++i) acc[16 * p + i] = __fmaf_rn(__uint_as_float(v[i]), sv, acc[16 * p + i]);
         }
         sl.next(kSlots);
-        ss.next(ring);
+        ss.next(kScaleSlots);
       }
       if (!ok) break;
       const Tile ti = tile_at<GROUPED>(g, table, t, half);
@@ -330,15 +350,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 template <bool GROUPED>
 int launch(const GemmArgs& g, int sm_count, cudaStream_t stream) {
   CUtensorMap tm_w, tm_a;
-  if (!make_code_map(&tm_w, g.w, (long long)g.E * g.N, g.K, 128)) return MOE_ERR_CUDA;
+  if (!make_code_map(&tm_w, g.w, (long long)g.E * g.N, g.K, 64)) return MOE_ERR_CUDA;
   if (!make_code_map(&tm_a, g.a, g.a_rows, g.K, GROUPED ? 1 : 128)) return MOE_ERR_CUDA;
   auto kern = wide_kernel<GROUPED>;
   const long long rows = GROUPED ? (long long)g.M / kRows + (g.E < g.M ? g.E : g.M) : ((long long)g.M - 1) / kRows + 1;
   const long long tiles = rows * ((g.nbn + 1) / 2);
   if (tiles >= (1LL << 31) - (1 << 16) || rows >= kMaxRowTiles) return MOE_ERR_CAPACITY;
-  const size_t extra = 1024 + kScaleBytes + (GROUPED ? (g.E + 1) * 4 : 0);
-  int stages = (int)((kMaxSmem - kStaticSmem - extra) / kStageBytes);
-  if (stages > kMaxStages) stages = kMaxStages;
+  static_assert(1024 + kStages * kStageBytes + kScaleBytes + (MOE_MAX_EXPERTS + 1) * 4 + kStaticSmem <= kMaxSmem, "");
   // All the shared memory a CTA may have: the pair holds both SMs' TMEM whole, so nothing
   // that allocates TMEM may share them.
   const size_t smem = kMaxSmem - kStaticSmem;
@@ -358,7 +376,7 @@ int launch(const GemmArgs& g, int sm_count, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_a, g, stages, (int)rows, vec) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_a, g, (int)rows, vec) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace

@@ -109,6 +109,26 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&v)[N]) {
 __device__ __forceinline__ void tcgen05_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tcgen05_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// mbar_wait for warps whose polling would take issue slots from others: the hardware may
+// suspend the thread for up to 1 ms a try, until the phase completes (bounded as mbar_wait).
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, uint32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    if (global_timer() - t0 > kWaitTimeoutNs) {
+      set_error(err, MOE_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // One lane of a converged warp (always the same one).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
