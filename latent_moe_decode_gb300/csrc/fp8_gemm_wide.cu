@@ -13,9 +13,9 @@
 //   - warps 17 and 18: MMA issuers, one for each half of the columns (in the pair's even
 //     CTA, for both): among the epilogue warps one warp's issue loop took longer than the
 //     multiplication it issues;
-//   - warp 19: scales. It walks the rows' scales ahead of the epilogue and leaves the
-//     products sa sw of a block, for both halves, in a ring in shared memory, so that
-//     the row-major scales are fetched once per CTA and not per warp.
+//   - warp 19: scales. It walks the rows' scales and leaves the products sa sw of a block
+//     in shared memory beside each half's TMEM slot (one barrier tells the epilogue of
+//     both), so that the row-major scales are fetched once per CTA and not per warp.
 // A persistent grid of pairs walks the tiles, row tiles of the same weights side by side.
 #include "fp8_gemm.cuh"
 
@@ -25,13 +25,15 @@ namespace {
 
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (kEpiWarps + 4);
+// Registers a thread: 96 at launch (65536 / 640, in eights); four warpgroups of epilogue
+// and one of the rest then share the same total, 4 * 104 + 64 = 5 * 96.
+constexpr int kEpiRegs = 104, kAuxRegs = 64;
 constexpr int kRows = 256, kCols = 256;       // a pair's tile
 constexpr int kHalf = 128 * FP8_BLOCK;        // bytes of one CTA's rows, or weights, of a stage
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kStages = 6;
 constexpr int kSlots = 2;                     // TMEM accumulators of each half of the columns: all 512 columns
-constexpr int kScaleSlots = 4;
-constexpr int kScaleBytes = kScaleSlots * 2 * 128 * 4;
+constexpr int kScaleBytes = kSlots * 2 * 128 * 4;
 
 struct Tile {
   int e, n0, pos, cnt;  // expert, first weight row, this CTA's first row and its rows (may be <= 0)
@@ -128,10 +130,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const GemmArgs g,
                 int max_row_tiles, int vec) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 4 * kSlots + 2 * kScaleSlots];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 6 * kSlots];
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sums[kThreads / 32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
   const int half = (int)cluster_rank();  // 0: the pair's leader
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const mem = smem_raw + (base - raw);
@@ -139,11 +141,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   int* const table = reinterpret_cast<int*>(mem + kStages * kStageBytes + kScaleBytes);
   auto full = [&](int i) { return smem_u32(&bars[i]); };  // (the leader's: both CTAs' bytes)
   auto empty = [&](int i) { return smem_u32(&bars[kStages + i]); };
-  // (slot, column half): the sums are there; they are read (the leader's: both CTAs' warps)
+  // (slot, column half): sums and scales are there; they are read, as the issuer (the
+  // leader's barrier: both CTAs' warps) and as the scale warp sees it
   auto tfull = [&](int i, int h) { return smem_u32(&bars[2 * kStages + 2 * i + h]); };
   auto tempty = [&](int i, int h) { return smem_u32(&bars[2 * kStages + 2 * kSlots + 2 * i + h]); };
-  auto sfull = [&](int i) { return smem_u32(&bars[2 * kStages + 4 * kSlots + i]); };
-  auto sempty = [&](int i) { return smem_u32(&bars[2 * kStages + 4 * kSlots + kScaleSlots + i]); };
+  auto sempty = [&](int i, int h) { return smem_u32(&bars[2 * kStages + 4 * kSlots + 2 * i + h]); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -151,12 +153,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(empty(i), 2);  // both issuers
     }
     for (int i = 0; i < 2 * kSlots; ++i) {
-      mbar_init(tfull(i >> 1, i & 1), 1);
+      mbar_init(tfull(i >> 1, i & 1), 2);           // the MMA's commit and the scale warp
       mbar_init(tempty(i >> 1, i & 1), kEpiWarps);  // half the epilogue warps of each CTA
-    }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(sfull(i), 1);
-      mbar_init(sempty(i), kEpiWarps);
+      mbar_init(sempty(i >> 1, i & 1), kEpiWarps / 2);
     }
     mbar_fence_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
@@ -183,151 +182,160 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   }
   const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-  if (warp == kEpiWarps) {  // TMA producer
-    Ring st;
-    int issued = 0;
-    const uint32_t lead = map_rank(full(0), 0);
-    bool ok = true;
-    for (int t = t0; t < tiles && ok; t += step) {
-      const Tile ti = tile_at<GROUPED>(g, table, t, half);
-      int r[4] = {0, 0, 0, 0};  // rows 4 lane .. 4 lane + 3 (row 0 for those past the end)
-      if constexpr (GROUPED) {
+  if (warp >= kEpiWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
+    if (warp == kEpiWarps) {  // TMA producer
+      Ring st;
+      int issued = 0;
+      const uint32_t lead = map_rank(full(0), 0);
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += step) {
+        const Tile ti = tile_at<GROUPED>(g, table, t, half);
+        int r[4] = {0, 0, 0, 0};  // rows 4 lane .. 4 lane + 3 (row 0 for those past the end)
+        if constexpr (GROUPED) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 4 * lane + i;
+            long long in = -1, out;
+            if (c < ti.cnt) pair_rows(g, ti.pos + c, &in, &out);
+            r[i] = in < 0 ? 0 : (int)in;
+          }
+        }
+        const int wrow = ti.e * g.N + ti.n0 + half * 64;
+        for (int kb = 0; kb < g.nbk; ++kb) {
+          ok = __all_sync(kFullMask, mbar_wait_asleep(empty(st.slot), st.lap ^ 1u, g.err));
+          if (!ok) break;
+          const uint32_t dst = base + st.slot * kStageBytes, bar = lead + 8 * st.slot;
+          if (elect_one()) {
+            if (half == 0) mbar_expect_tx(full(st.slot), 2 * kStageBytes);
+            tma_load_2d_pair(dst + kHalf, &tm_w, kb * FP8_BLOCK, wrow, bar);
+            tma_load_2d_pair(dst + kHalf + kHalf / 2, &tm_w, kb * FP8_BLOCK, wrow + 128, bar);
+            if (!GROUPED) tma_load_2d_pair(dst, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
+          }
+          __syncwarp();
+          if (GROUPED) tma_gather4_pair(dst + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
+          st.next(kStages);
+          ++issued;
+        }
+      }
+      // the pair's copies still in flight land before either CTA may exit
+      if (half == 0)
+        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+          mbar_wait_asleep(full(i % kStages), (uint32_t)(i / kStages) & 1u, g.err);
+    } else if (warp == kEpiWarps + 1 || warp == kEpiWarps + 2) {  // MMA issuers
+      // (the whole warp walks the loop, so that descriptors stay in uniform registers)
+      if (half == 0) {
+        constexpr uint32_t idesc = instr_desc_e4m3(kCols / 2, kRows);
+        const int h = warp - kEpiWarps - 1;
+        const uint64_t rows0 = sw128_desc(base), weights0 = sw128_desc(base + kHalf + h * (kHalf / 2));
+        Ring st;
+        uint32_t laps = 0;  // bit i: the lap of TMEM slot i (a tile's blocks take the slots in turn from 0)
+        bool ok = true;
+        for (int t = t0; t < tiles && ok; t += step) {
+          for (int kb = 0; kb < g.nbk; ++kb) {
+            const int sl = kb & 1;
+            ok = __all_sync(kFullMask, mbar_wait_asleep(tempty(sl, h), ((laps >> sl) & 1u) ^ 1u, g.err) &&
+                                           mbar_wait_asleep(full(st.slot), st.lap, g.err));
+            if (!ok) break;
+            tcgen05_after_sync();
+            const uint64_t at = (uint64_t)(st.slot * (kStageBytes >> 4));
+            const uint32_t d = tmem + sl * kCols + h * (kCols / 2);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_e4m3_pair(d, rows0 + at + 2 * k, weights0 + at + 2 * k, idesc, k > 0 ? 1u : 0u);
+              mma_commit_pair(tfull(sl, h), (uint16_t)3);
+              mma_commit_pair(empty(st.slot), (uint16_t)3);
+            }
+            __syncwarp();
+            st.next(kStages);
+            laps ^= 1u << sl;
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == kEpiWarps + 3) {  // scales
+      uint32_t laps = 0;
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += step) {
+        const Tile ti = tile_at<GROUPED>(g, table, t, half);
+        const float* sap[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = 4 * lane + i;
           long long in = -1, out;
-          if (c < ti.cnt) pair_rows(g, ti.pos + c, &in, &out);
-          r[i] = in < 0 ? 0 : (int)in;
-        }
-      }
-      const int wrow = ti.e * g.N + ti.n0 + half * 64;
-      for (int kb = 0; kb < g.nbk; ++kb) {
-        ok = __all_sync(kFullMask, mbar_wait_asleep(empty(st.slot), st.lap ^ 1u, g.err));
-        if (!ok) break;
-        const uint32_t dst = base + st.slot * kStageBytes, bar = lead + 8 * st.slot;
-        if (elect_one()) {
-          if (half == 0) mbar_expect_tx(full(st.slot), 2 * kStageBytes);
-          tma_load_2d_pair(dst + kHalf, &tm_w, kb * FP8_BLOCK, wrow, bar);
-          tma_load_2d_pair(dst + kHalf + kHalf / 2, &tm_w, kb * FP8_BLOCK, wrow + 128, bar);
-          if (!GROUPED) tma_load_2d_pair(dst, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
-        }
-        __syncwarp();
-        if (GROUPED) tma_gather4_pair(dst + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
-        st.next(kStages);
-        ++issued;
-      }
-    }
-    // the pair's copies still in flight land before either CTA may exit
-    if (half == 0)
-      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-        mbar_wait_asleep(full(i % kStages), (uint32_t)(i / kStages) & 1u, g.err);
-  } else if (warp == kEpiWarps + 1 || warp == kEpiWarps + 2) {  // MMA issuers
-    // (the whole warp walks the loop, so that descriptors stay in uniform registers)
-    if (half == 0) {
-      constexpr uint32_t idesc = instr_desc_e4m3(kCols / 2, kRows);
-      const int h = warp - kEpiWarps - 1;
-      const uint64_t rows0 = sw128_desc(base), weights0 = sw128_desc(base + kHalf + h * (kHalf / 2));
-      Ring st, sl;
-      bool ok = true;
-      for (int t = t0; t < tiles && ok; t += step) {
-        for (int kb = 0; kb < g.nbk; ++kb) {
-          ok = __all_sync(kFullMask, mbar_wait_asleep(tempty(sl.slot, h), sl.lap ^ 1u, g.err) && mbar_wait_asleep(full(st.slot), st.lap, g.err));
-          if (!ok) break;
-          tcgen05_after_sync();
-          const uint64_t at = (uint64_t)(st.slot * (kStageBytes >> 4));
-          const uint32_t d = tmem + sl.slot * kCols + h * (kCols / 2);
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_e4m3_pair(d, rows0 + at + 2 * k, weights0 + at + 2 * k, idesc, k > 0 ? 1u : 0u);
-            mma_commit_pair(tfull(sl.slot, h), (uint16_t)3);
-            mma_commit_pair(empty(st.slot), (uint16_t)3);
+          if (c < ti.cnt) {
+            if constexpr (GROUPED)
+              pair_rows(g, ti.pos + c, &in, &out);
+            else
+              in = ti.pos + c;
           }
+          sap[i] = in < 0 ? nullptr : g.sa + in * g.nbk;
+        }
+        const int wb = ti.n0 / FP8_BLOCK;
+        const float* sw0 = g.sw + ((long long)ti.e * g.nbn + wb) * g.nbk;
+        const int next = wb + 1 < g.nbn ? g.nbk : 0;  // to the second half's scales
+        float s[4], b0 = 0.f, b1 = 0.f;
+        auto fetch = [&](int kb) {
+          b0 = __ldg(sw0 + kb);
+          b1 = __ldg(sw0 + next + kb);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] = sap[i] ? __ldg(sap[i] + kb) : 0.f;
+        };
+        fetch(0);
+        for (int kb = 0; kb < g.nbk; ++kb) {
+          const int sl = kb & 1;
+          const uint32_t lap = ((laps >> sl) & 1u) ^ 1u;
+          ok = __all_sync(kFullMask, mbar_wait_asleep(sempty(sl, 0), lap, g.err) && mbar_wait_asleep(sempty(sl, 1), lap, g.err));
+          if (!ok) break;
+          float4* d = reinterpret_cast<float4*>(scale_mem + sl * 256) + lane;
+          d[0] = make_float4(__fmul_rn(s[0], b0), __fmul_rn(s[1], b0), __fmul_rn(s[2], b0), __fmul_rn(s[3], b0));
+          d[32] = make_float4(__fmul_rn(s[0], b1), __fmul_rn(s[1], b1), __fmul_rn(s[2], b1), __fmul_rn(s[3], b1));
           __syncwarp();
-          st.next(kStages);
-          sl.next(kSlots);
+          if (lane < 2) mbar_arrive(tfull(sl, lane));
+          if (kb + 1 < g.nbk) fetch(kb + 1);
+          laps ^= 1u << sl;
         }
-      }
-    }
-    __syncwarp();
-  } else if (warp == kEpiWarps + 3) {  // scales
-    Ring sc;
-    bool ok = true;
-    for (int t = t0; t < tiles && ok; t += step) {
-      const Tile ti = tile_at<GROUPED>(g, table, t, half);
-      const float* sap[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = 4 * lane + i;
-        long long in = -1, out;
-        if (c < ti.cnt) {
-          if constexpr (GROUPED)
-            pair_rows(g, ti.pos + c, &in, &out);
-          else
-            in = ti.pos + c;
-        }
-        sap[i] = in < 0 ? nullptr : g.sa + in * g.nbk;
-      }
-      const int wb = ti.n0 / FP8_BLOCK;
-      const float* sw0 = g.sw + ((long long)ti.e * g.nbn + wb) * g.nbk;
-      const int next = wb + 1 < g.nbn ? g.nbk : 0;  // to the second half's scales
-      float s[4], b0 = 0.f, b1 = 0.f;
-      auto fetch = [&](int kb) {
-        b0 = __ldg(sw0 + kb);
-        b1 = __ldg(sw0 + next + kb);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = sap[i] ? __ldg(sap[i] + kb) : 0.f;
-      };
-      fetch(0);
-      for (int kb = 0; kb < g.nbk; ++kb) {
-        ok = __all_sync(kFullMask, mbar_wait_asleep(sempty(sc.slot), sc.lap ^ 1u, g.err));
-        if (!ok) break;
-        float4* d = reinterpret_cast<float4*>(scale_mem + sc.slot * 256) + lane;
-        d[0] = make_float4(__fmul_rn(s[0], b0), __fmul_rn(s[1], b0), __fmul_rn(s[2], b0), __fmul_rn(s[3], b0));
-        d[32] = make_float4(__fmul_rn(s[0], b1), __fmul_rn(s[1], b1), __fmul_rn(s[2], b1), __fmul_rn(s[3], b1));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sfull(sc.slot));
-        if (kb + 1 < g.nbk) fetch(kb + 1);
-        sc.next(kScaleSlots);
       }
     }
   } else {  // epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int q = warp & 3, cg = warp >> 2, h = cg >> 1, row = q * 32 + lane;  // half h of the columns
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + cg * 64;
     const float* const sc = scale_mem + h * 128 + row;
     const uint32_t lead = map_rank(tempty(0, h), 0);  // the leader's; the next slot's is 16 bytes on
-    Ring sl, ss;  // TMEM and scale slots
+    uint32_t laps = 0;
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       float acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0.f;
-      for (int kb = 0; kb < g.nbk; ++kb) {
-        ok = mbar_wait_asleep(sfull(ss.slot), ss.lap, g.err);
-        const float sv = sc[ss.slot * 256];
-        ok = __all_sync(kFullMask, ok && mbar_wait_asleep(tfull(sl.slot, h), sl.lap, g.err));
-        if (!ok) break;
+      auto fold = [&](const int sl) {  // one block's sums, from slot sl
+        ok = __all_sync(kFullMask, mbar_wait_asleep(tfull(sl, h), (laps >> sl) & 1u, g.err));
+        laps ^= 1u << sl;
         tcgen05_after_sync();
-        const uint32_t col = tl + sl.slot * kCols;
+        const float sv = sc[sl * 256];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           uint32_t v[16];
-          tmem_ld16(col + 16 * p, v);
+          tmem_ld16(tl + sl * kCols + 16 * p, v);
           tmem_wait_ld();
           tmem_loaded(v);
           if (p == 3) {  // the slot is read
             tcgen05_before_sync();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive_cluster(lead + 16 * sl.slot);
-              mbar_arrive(sempty(ss.slot));
+              mbar_arrive_cluster(lead + 16 * sl);
+              mbar_arrive(sempty(sl, h));
             }
           }
           // (FFMA and not the packed form, whose operand pairs cost two moves each here)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[16 * p + i] = __fmaf_rn(__uint_as_float(v[i]), sv, acc[16 * p + i]);
         }
-        sl.next(kSlots);
-        ss.next(kScaleSlots);
+      };
+      for (int kb = 0; kb < g.nbk && ok; kb += 2) {
+        fold(0);
+        if (kb + 1 < g.nbk && ok) fold(1);
       }
       if (!ok) break;
       const Tile ti = tile_at<GROUPED>(g, table, t, half);
