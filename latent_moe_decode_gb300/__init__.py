@@ -25,6 +25,7 @@ __all__ = [
     "ROUTER_AUTO", "ROUTER_SIMT", "ROUTER_TCGEN05", "MXFP8_SCALE_FLOOR", "MXFP8_SCALE_CEIL",
     "DEVERR_ROW_INDEX", "DEVERR_EXPERT_ID", "DEVERR_TIMEOUT", "DEVERR_CAPACITY",
     "topk_route_grouped", "fp8_block_quantize_rows", "fp8_block_quantize_swiglu", "fp8_block_gemm", "expert_gemm",
+    "expert_gemm_workspace",
     "block_norm", "FP8_BLOCK", "SCORE_SIGMOID", "SCORE_SOFTMAX", "GROUP_MAX", "GROUP_TOP2", "FP8_SCALE_AMAX",
     "FP8_SCALE_POW2", "ROWS_TOKEN", "ROWS_LIST", "ROWS_PAIR",
 ]
@@ -71,7 +72,8 @@ SIGNATURES = {
     "fp8_block_quantize_rows": (_I, [_P, _L, _I, _I, _P, _P, _I, _P]),
     "fp8_block_quantize_swiglu": (_I, [_P, _L, _I, _I, _P, _P, _I, _P]),
     "fp8_block_gemm": (_I, [_P] * 5 + [_I] * 4 + [_P]),
-    "moe_expert_gemm": (_I, [_P, _P, _L, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P]),
+    "moe_expert_gemm_workspace": (_SZ, [_I, _I, _I, _I]),
+    "moe_expert_gemm": (_I, [_P, _P, _L, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P, _SZ, _P]),
     "moe_block_norm": (_I, [_P, _L, _P, _I, _P, _P, _I, _P, _F, _F, _I, _I, _P, _P, _P, _P, _P]),
 }
 
@@ -483,8 +485,12 @@ def fp8_block_gemm(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16,
     return out
 
 
+def expert_gemm_workspace(n_pairs: int, E: int, K: int, in_rows: int = ROWS_TOKEN) -> int:
+    return int(load().moe_expert_gemm_workspace(n_pairs, E, K, in_rows))
+
+
 def expert_gemm(a, a_scales, w, w_scales, offsets, pairs, topk: int, in_rows: int = ROWS_TOKEN,
-                out_rows: int = ROWS_PAIR, out=None, out_dtype=torch.bfloat16, stream=None):
+                out_rows: int = ROWS_PAIR, out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
     """out [n_pairs, N] (BF16 or FP32): every listed pair's row of codes a times its expert's
     weights w [E, N, K]^T, over the lists of build_routing_lists (offsets [E+1], pairs).
     in_rows: which row of a a pair multiplies (ROWS_TOKEN, ROWS_LIST, ROWS_PAIR); out_rows:
@@ -500,9 +506,13 @@ def expert_gemm(a, a_scales, w, w_scales, offsets, pairs, topk: int, in_rows: in
     _need(pairs, torch.int32, (P,), "pairs")
     dt, code = _out_dtype(out, out_dtype)
     out = _empty((P, N), dt, a) if out is None else _need(out, dt, (P, N), "out")
+    need = expert_gemm_workspace(P, E, K, in_rows)
+    if need and workspace is None:
+        workspace = _empty((need,), torch.uint8, a)
+    wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("moe_expert_gemm", load().moe_expert_gemm(
         _ptr(a), _ptr(a_scales), a_rows, _ptr(w), _ptr(w_scales), _ptr(offsets), _ptr(pairs), P, int(topk), int(in_rows),
-        int(out_rows), _ptr(out), code, E, N, K, _stream(stream)))
+        int(out_rows), _ptr(out), code, E, N, K, _ptr(workspace), wb, _stream(stream)))
     return out
 
 

@@ -18,15 +18,63 @@ int check(const GemmArgs& a, int out_dtype) {
   return MOE_OK;
 }
 
-int launch(GemmArgs& a, cudaStream_t stream) {
+// Which kernel. Measured (N = 7168, K = 3584) ...
+bool wide(const GemmArgs& a) { return a.offsets ? (long long)a.M >= 96LL * a.E : a.M >= 256; }
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Copies of the listed pairs' rows and scales in list order.
+size_t list_copy_bytes(int n_pairs, int K) {
+  return align256((size_t)n_pairs * K) + align256((size_t)n_pairs * ((K - 1) / FP8_BLOCK + 1) * sizeof(float));
+}
+
+constexpr int kCopyThreads = 256;
+
+// One warp per list position: K bytes of codes in 16-byte pieces, and the row's scales.
+// (Bound by the copies' bytes; a token's row is read topk times, from L2.)
+__global__ void __launch_bounds__(kCopyThreads) list_copy_kernel(const GemmArgs g, uint8_t* __restrict__ a,
+                                                                 float* __restrict__ sa) {
+  grid_launch_dependents();
+  grid_wait();
+  const int lane = threadIdx.x & 31, warps = gridDim.x * (kCopyThreads / 32);
+  const int end = fp8_impl::clamp_offset(__ldg(g.offsets + g.E), g.M);
+  for (int i = (blockIdx.x * kCopyThreads + threadIdx.x) >> 5; i < end; i += warps) {
+    long long in, out;
+    fp8_impl::pair_rows(g, i, &in, &out);
+    if (in < 0) continue;  // (its product is not stored)
+    const uint4* src = reinterpret_cast<const uint4*>(g.a + in * g.K);
+    uint4* dst = reinterpret_cast<uint4*>(a + (long long)i * g.K);
+    for (int c = lane; c < g.K / 16; c += 32 * 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c + 32 * u < g.K / 16) v[u] = __ldg(src + c + 32 * u);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c + 32 * u < g.K / 16) dst[c + 32 * u] = v[u];
+    }
+    for (int b = lane; b < g.nbk; b += 32) sa[(long long)i * g.nbk + b] = __ldg(g.sa + in * g.nbk + b);
+  }
+}
+
+int launch(GemmArgs& a, void* workspace, cudaStream_t stream) {
   if ((long long)a.E * a.N > 0x7FFFFFFFLL - 128 || a.a_rows > 0x7FFFFFFFLL) return MOE_ERR_CAPACITY;  // (TMA coordinates)
   a.nbk = (a.K - 1) / FP8_BLOCK + 1, a.nbn = (a.N - 1) / FP8_BLOCK + 1;
   DeviceInfo dev;
   int st = current_device(&dev);
   if (st != MOE_OK) return st;
   a.err = dev.error_word;
-  const bool wide = a.offsets ? (long long)a.M >= 96LL * a.E : a.M >= 256;
-  return wide ? fp8_impl::launch_wide(a, dev.sm_count, stream) : fp8_impl::launch_narrow(a, dev.sm_count, stream);
+  if (!wide(a)) return fp8_impl::launch_narrow(a, dev.sm_count, stream);
+  if (a.offsets && a.in_rows != MOE_ROWS_LIST) {
+    uint8_t* rows = static_cast<uint8_t*>(workspace);
+    float* scales = reinterpret_cast<float*>(rows + align256((size_t)a.M * a.K));
+    const long long need = ((long long)a.M * 32 + kCopyThreads - 1) / kCopyThreads, most = 8LL * dev.sm_count;
+    st = launch_pdl(list_copy_kernel, dim3((unsigned)(need < most ? need : most)), dim3(kCopyThreads), 0, stream, a, rows, scales);
+    if (st != MOE_OK) return st;
+    a.a = rows, a.sa = scales;
+    return fp8_impl::launch_wide(a, a.M, dev.sm_count, stream);
+  }
+  return fp8_impl::launch_wide(a, a.a_rows, dev.sm_count, stream);
 }
 
 }  // namespace
@@ -40,13 +88,21 @@ extern "C" int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uin
   g.M = M, g.N = N, g.K = K, g.E = 1, g.a_rows = M;
   const int st = check(g, out_dtype);
   if (st != MOE_OK || M == 0 || N == 0) return st;
-  return launch(g, as_cuda(stream));
+  return launch(g, nullptr, as_cuda(stream));
+}
+
+extern "C" size_t moe_expert_gemm_workspace(int n_pairs, int E, int K, int in_rows) {
+  moe::GemmArgs g = {};
+  static const int32_t listed = 0;
+  g.offsets = &listed, g.M = n_pairs, g.E = E;
+  if (n_pairs < 1 || E < 1 || K < 16 || in_rows == MOE_ROWS_LIST || !moe::wide(g)) return 0;
+  return moe::list_copy_bytes(n_pairs, K);
 }
 
 extern "C" int moe_expert_gemm(const uint8_t* a, const float* a_scales, int64_t a_rows, const uint8_t* w,
                                const float* w_scales, const int32_t* offsets, const int32_t* pairs, int n_pairs,
                                int topk, int in_rows, int out_rows, void* out, int out_dtype, int E, int N, int K,
-                               moe_stream_t stream) {
+                               void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   using namespace moe;
   GemmArgs g = {};
   g.a = a, g.sa = a_scales, g.w = w, g.sw = w_scales, g.out = out, g.f32 = out_dtype == MOE_DTYPE_F32;
@@ -59,6 +115,8 @@ extern "C" int moe_expert_gemm(const uint8_t* a, const float* a_scales, int64_t 
   if (st != MOE_OK || n_pairs == 0 || N == 0) return st;
   if (!offsets || !pairs) return MOE_ERR_INVALID_ARGUMENT;
   if (E > MOE_MAX_EXPERTS) return MOE_ERR_CAPACITY;
-  if (!aligned(offsets, 4) || !aligned(pairs, 4)) return MOE_ERR_ALIGNMENT;
-  return launch(g, as_cuda(stream));
+  if (!aligned(offsets, 4) || !aligned(pairs, 4) || !aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
+  if (workspace_bytes < moe_expert_gemm_workspace(n_pairs, E, K, in_rows)) return MOE_ERR_WORKSPACE;
+  if (!workspace && moe_expert_gemm_workspace(n_pairs, E, K, in_rows) > 0) return MOE_ERR_WORKSPACE;
+  return launch(g, workspace, as_cuda(stream));
 }

@@ -30,7 +30,9 @@ struct GemmArgs {
 // Few rows per weight tile: weights on the tensor core's 128 lanes, rows on its columns.
 int launch_narrow(const GemmArgs& g, int sm_count, cudaStream_t stream);
 // Many rows per weight tile: rows on the lanes, weights on the columns, two SMs per tile.
-int launch_wide(const GemmArgs& g, int sm_count, cudaStream_t stream);
+// Grouped, g.a and g.sa hold the rows in list order, `rows` of them (in_rows and a_rows
+// say which rows of the caller's they are, and so which pairs are in range).
+int launch_wide(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream);
 
 // A K-major byte matrix [rows, cols] for TMA: boxes of 128 columns x box_rows rows,
 // 128-byte swizzle, zeros outside.

@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * C::kSlots];
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sums[kThreads / 32];
+  __shared__ int4 row_mem[GROUPED ? BN / 4 : 1];  // the rows of a tile, four per gather
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const mem = smem_raw + (base - raw);
@@ -127,8 +128,8 @@ __global__ void __launch_bounds__(kThreads)
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       const Tile ti = tile_at<BN, GROUPED>(g, table, t);
-      int r[4] = {0, 0, 0, 0};  // rows 4 lane .. 4 lane + 3 of the tile (row 0 for those past its end)
       if constexpr (GROUPED) {
+        int r[4];  // rows 4 lane .. 4 lane + 3 of the tile (row 0 for those past its end)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = 4 * lane + i;
@@ -136,6 +137,8 @@ __global__ void __launch_bounds__(kThreads)
           if (c < ti.cnt) pair_rows(g, ti.pos + c, &in, &out);
           r[i] = in < 0 ? 0 : (int)in;
         }
+        if (lane < BN / 4) row_mem[lane] = make_int4(r[0], r[1], r[2], r[3]);
+        __syncwarp();
       }
       const int wrow = ti.e * g.N + ti.n0;
       for (int kb = kb0; kb < kb1; ++kb) {
@@ -145,11 +148,17 @@ __global__ void __launch_bounds__(kThreads)
         if (elect_one()) {
           mbar_expect_tx(bar, C::kStageBytes);
           tma_load_2d(dst, &tm_w, kb * FP8_BLOCK, wrow, bar);
-          if (!GROUPED) tma_load_2d(dst + kWBytes, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
+          if constexpr (GROUPED) {  // (by one thread: per lane the instruction is issued lane after lane)
+#pragma unroll 8
+            for (int j = 0; j < BN / 4; ++j) {
+              const int4 r = row_mem[j];
+              tma_gather4(dst + kWBytes + j * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r.x, r.y, r.z, r.w, bar);
+            }
+          } else {
+            tma_load_2d(dst + kWBytes, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
+          }
         }
         __syncwarp();
-        if (GROUPED && lane < BN / 4)
-          tma_gather4(dst + kWBytes + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
         st.next(stages);
         ++issued;
       }

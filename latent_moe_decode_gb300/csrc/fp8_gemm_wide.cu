@@ -9,7 +9,7 @@
 // half multiplies. With the rows on the lanes a thread's scale is one number for a half:
 //   - warps 0-15: epilogue. Warp w reads lanes 32 (w % 4).. and columns 64 (w / 4).. and
 //     folds each block's sums, times its scale, into 64 FP32 registers a thread;
-//   - warp 16: TMA producer (rows of an expert's list by gather4, four at a time);
+//   - warp 16: TMA producer;
 //   - warps 17 and 18: MMA issuers, one for each half of the columns (in the pair's even
 //     CTA, for both): among the epilogue warps one warp's issue loop took longer than the
 //     multiplication it issues;
@@ -17,6 +17,11 @@
 //     in shared memory beside each half's TMEM slot (one barrier tells the epilogue of
 //     both), so that the row-major scales are fetched once per CTA and not per warp.
 // A persistent grid of pairs walks the tiles, row tiles of the same weights side by side.
+// Grouped, the rows of an expert's list are read as one box, so they have to lie in list
+// order: launch_wide copies rows that do not (MOE_ROWS_TOKEN, MOE_ROWS_PAIR) there first.
+// (TMA's gather4, which could fetch them from where they are, moved 128 rows x 128 bytes
+// in 2300 cycles, against 900 for a whole block with the copies: 4096 tokens x 8 of 64
+// experts took 1166 us with it.)
 #include "fp8_gemm.cuh"
 
 namespace moe {
@@ -26,8 +31,8 @@ namespace {
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (kEpiWarps + 4);
 // Registers a thread: 96 at launch (65536 / 640, in eights); four warpgroups of epilogue
-// and one of the rest then share the same total, 4 * 104 + 64 = 5 * 96.
-constexpr int kEpiRegs = 104, kAuxRegs = 64;
+// and one of the rest then share the same total, 4 * 112 + 32 = 5 * 96.
+constexpr int kEpiRegs = 112, kAuxRegs = 32;
 constexpr int kRows = 256, kCols = 256;       // a pair's tile
 constexpr int kHalf = 128 * FP8_BLOCK;        // bytes of one CTA's rows, or weights, of a stage
 constexpr int kStageBytes = 2 * kHalf;
@@ -64,15 +69,6 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t tmem_d, uint64_t adesc, u
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc));
-}
-
-__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* map, int c0, int r0, int r1, int r2,
-                                                 int r3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-      "%3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-      : "memory");
 }
 
 // Arrive on a barrier of the cluster (a shared::cluster address). Relaxed: what it reports is a
@@ -128,7 +124,7 @@ __device__ __forceinline__ void store_row(const GemmArgs& g, long long row, int 
 template <bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const GemmArgs g,
-                int max_row_tiles, int vec) {
+                long long rows, int max_row_tiles, int vec) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 6 * kSlots];
   __shared__ uint32_t tmem_slot;
@@ -191,16 +187,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += step) {
         const Tile ti = tile_at<GROUPED>(g, table, t, half);
-        int r[4] = {0, 0, 0, 0};  // rows 4 lane .. 4 lane + 3 (row 0 for those past the end)
-        if constexpr (GROUPED) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = 4 * lane + i;
-            long long in = -1, out;
-            if (c < ti.cnt) pair_rows(g, ti.pos + c, &in, &out);
-            r[i] = in < 0 ? 0 : (int)in;
-          }
-        }
         const int wrow = ti.e * g.N + ti.n0 + half * 64;
         for (int kb = 0; kb < g.nbk; ++kb) {
           ok = __all_sync(kFullMask, mbar_wait_asleep(empty(st.slot), st.lap ^ 1u, g.err));
@@ -210,10 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (half == 0) mbar_expect_tx(full(st.slot), 2 * kStageBytes);
             tma_load_2d_pair(dst + kHalf, &tm_w, kb * FP8_BLOCK, wrow, bar);
             tma_load_2d_pair(dst + kHalf + kHalf / 2, &tm_w, kb * FP8_BLOCK, wrow + 128, bar);
-            if (!GROUPED) tma_load_2d_pair(dst, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
+            tma_load_2d_pair(dst, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
           }
           __syncwarp();
-          if (GROUPED) tma_gather4_pair(dst + lane * 4 * FP8_BLOCK, &tm_a, kb * FP8_BLOCK, r[0], r[1], r[2], r[3], bar);
           st.next(kStages);
           ++issued;
         }
@@ -234,17 +219,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int t = t0; t < tiles && ok; t += step) {
           for (int kb = 0; kb < g.nbk; ++kb) {
             const int sl = kb & 1;
-            ok = __all_sync(kFullMask, mbar_wait_asleep(tempty(sl, h), ((laps >> sl) & 1u) ^ 1u, g.err) &&
-                                           mbar_wait_asleep(full(st.slot), st.lap, g.err));
+            const uint32_t at = st.slot * (kStageBytes >> 4), d = tmem + sl * kCols + h * (kCols / 2);
+            const uint64_t rd = rows0 + at, wd = weights0 + at;
+            const uint32_t done = tfull(sl, h), used = empty(st.slot);
+            ok = __all_sync(kFullMask, mbar_wait_asleep(full(st.slot), st.lap, g.err) &&
+                                           mbar_wait_asleep(tempty(sl, h), ((laps >> sl) & 1u) ^ 1u, g.err));
             if (!ok) break;
             tcgen05_after_sync();
-            const uint64_t at = (uint64_t)(st.slot * (kStageBytes >> 4));
-            const uint32_t d = tmem + sl * kCols + h * (kCols / 2);
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_e4m3_pair(d, rows0 + at + 2 * k, weights0 + at + 2 * k, idesc, k > 0 ? 1u : 0u);
-              mma_commit_pair(tfull(sl, h), (uint16_t)3);
-              mma_commit_pair(empty(st.slot), (uint16_t)3);
+              for (int k = 0; k < 4; ++k) mma_e4m3_pair(d, rd + 2 * k, wd + 2 * k, idesc, k > 0 ? 1u : 0u);
+              mma_commit_pair(done, (uint16_t)3);
+              mma_commit_pair(used, (uint16_t)3);
             }
             __syncwarp();
             st.next(kStages);
@@ -258,19 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += step) {
         const Tile ti = tile_at<GROUPED>(g, table, t, half);
-        const float* sap[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 4 * lane + i;
-          long long in = -1, out;
-          if (c < ti.cnt) {
-            if constexpr (GROUPED)
-              pair_rows(g, ti.pos + c, &in, &out);
-            else
-              in = ti.pos + c;
-          }
-          sap[i] = in < 0 ? nullptr : g.sa + in * g.nbk;
-        }
+        // rows 4 lane .. 4 lane + 3 of the tile, those of them that there are
+        const float* sa = g.sa + ((long long)ti.pos + 4 * lane) * g.nbk;
+        const int n = (int)min((long long)ti.cnt, rows - ti.pos) - 4 * lane;
         const int wb = ti.n0 / FP8_BLOCK;
         const float* sw0 = g.sw + ((long long)ti.e * g.nbn + wb) * g.nbk;
         const int next = wb + 1 < g.nbn ? g.nbk : 0;  // to the second half's scales
@@ -279,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           b0 = __ldg(sw0 + kb);
           b1 = __ldg(sw0 + next + kb);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[i] = sap[i] ? __ldg(sap[i] + kb) : 0.f;
+          for (int i = 0; i < 4; ++i) s[i] = i < n ? __ldg(sa + (long long)i * g.nbk + kb) : 0.f;
         };
         fetch(0);
         for (int kb = 0; kb < g.nbk; ++kb) {
@@ -315,12 +291,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tcgen05_after_sync();
         const float sv = sc[sl * 256];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          uint32_t v[16];
-          tmem_ld16(tl + sl * kCols + 16 * p, v);
+        for (int p = 0; p < 2; ++p) {
+          uint32_t v[32];
+          tmem_ld32(tl + sl * kCols + 32 * p, v);
           tmem_wait_ld();
           tmem_loaded(v);
-          if (p == 3) {  // the slot is read
+          if (p == 1) {  // the slot is read
             tcgen05_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -330,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           }
           // (FFMA and not the packed form, whose operand pairs cost two moves each here)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[16 * p + i] = __fmaf_rn(__uint_as_float(v[i]), sv, acc[16 * p + i]);
+          for (int i = 0; i < 32; ++i) acc[32 * p + i] = __fmaf_rn(__uint_as_float(v[i]), sv, acc[32 * p + i]);
         }
       };
       for (int kb = 0; kb < g.nbk && ok; kb += 2) {
@@ -356,10 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 template <bool GROUPED>
-int launch(const GemmArgs& g, int sm_count, cudaStream_t stream) {
+int launch(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t stream) {
   CUtensorMap tm_w, tm_a;
   if (!make_code_map(&tm_w, g.w, (long long)g.E * g.N, g.K, 64)) return MOE_ERR_CUDA;
-  if (!make_code_map(&tm_a, g.a, g.a_rows, g.K, GROUPED ? 1 : 128)) return MOE_ERR_CUDA;
+  if (!make_code_map(&tm_a, g.a, a_rows, g.K, 128)) return MOE_ERR_CUDA;
   auto kern = wide_kernel<GROUPED>;
   const long long rows = GROUPED ? (long long)g.M / kRows + (g.E < g.M ? g.E : g.M) : ((long long)g.M - 1) / kRows + 1;
   const long long tiles = rows * ((g.nbn + 1) / 2);
@@ -384,13 +360,13 @@ int launch(const GemmArgs& g, int sm_count, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_a, g, (int)rows, vec) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_a, g, a_rows, (int)rows, vec) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
 
-int launch_wide(const GemmArgs& g, int sm_count, cudaStream_t stream) {
-  return g.offsets ? launch<true>(g, sm_count, stream) : launch<false>(g, sm_count, stream);
+int launch_wide(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream) {
+  return g.offsets ? launch<true>(g, rows, sm_count, stream) : launch<false>(g, rows, sm_count, stream);
 }
 
 }  // namespace fp8_impl

@@ -303,6 +303,27 @@ def test_expert_gemm_skips_bad_pairs(moe):
     assert moe.device_error() == moe.DEVERR_ROW_INDEX
 
 
+def test_expert_gemm_skips_bad_pairs_of_long_lists(moe):
+    """The same where lists are long (rows in list order are another path)."""
+    T, topk, E, N, K = 200, 2, 2, 140, 160
+    rng = np.random.default_rng(9)
+    a, sa, w, sw = operands(1, T, N, K, experts=E)
+    offsets, pairs = lists(rng.integers(0, E, (T, topk)), E)
+    pairs[7], pairs[300] = -9, T * topk
+    for in_rows, known in ((moe.ROWS_TOKEN, 150), (moe.ROWS_PAIR, 200), (moe.ROWS_LIST, 200)):
+        out = torch.full((T * topk, N), 3.0, device="cuda")
+        moe.expert_gemm(dev(a[:known]), dev(sa[:known]), dev(w), dev(sw), dev(offsets), dev(pairs), topk, in_rows=in_rows, out=out)
+        assert moe.device_error() == moe.DEVERR_ROW_INDEX
+        written = np.zeros(T * topk, bool)
+        for e in range(E):
+            pos = np.arange(offsets[e], offsets[e + 1])
+            src = {moe.ROWS_TOKEN: pairs[pos] // topk, moe.ROWS_LIST: pos, moe.ROWS_PAIR: pairs[pos]}[in_rows]
+            ok = (src >= 0) & (src < known) & (pairs[pos] >= 0) & (pairs[pos] < T * topk)
+            written[pairs[pos][ok]] = True
+            gemm_check(out[torch.from_numpy(pairs[pos][ok].astype(np.int64)).cuda()], a[src[ok]], sa[src[ok]], w[e], sw[e])
+        assert (out[torch.from_numpy(~written).cuda()] == 3.0).all()
+
+
 def test_expert_gemm_bad_offsets(moe):
     """Offsets past the list's ends, or descending, count as the nearest bound or as empty lists."""
     T, topk, E, N, K = 12, 2, 5, 64, 64
