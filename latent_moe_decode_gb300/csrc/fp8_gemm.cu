@@ -64,17 +64,16 @@ int launch(GemmArgs& a, void* workspace, cudaStream_t stream) {
   int st = current_device(&dev);
   if (st != MOE_OK) return st;
   a.err = dev.error_word;
-  if (!wide(a)) return fp8_impl::launch_narrow(a, dev.sm_count, stream);
+  long long rows = a.a_rows;
   if (a.offsets && a.in_rows != MOE_ROWS_LIST) {
-    uint8_t* rows = static_cast<uint8_t*>(workspace);
-    float* scales = reinterpret_cast<float*>(rows + align256((size_t)a.M * a.K));
+    uint8_t* copy = static_cast<uint8_t*>(workspace);
+    float* scales = reinterpret_cast<float*>(copy + align256((size_t)a.M * a.K));
     const long long need = ((long long)a.M * 32 + kCopyThreads - 1) / kCopyThreads, most = 8LL * dev.sm_count;
-    st = launch_pdl(list_copy_kernel, dim3((unsigned)(need < most ? need : most)), dim3(kCopyThreads), 0, stream, a, rows, scales);
+    st = launch_pdl(list_copy_kernel, dim3((unsigned)(need < most ? need : most)), dim3(kCopyThreads), 0, stream, a, copy, scales);
     if (st != MOE_OK) return st;
-    a.a = rows, a.sa = scales;
-    return fp8_impl::launch_wide(a, a.M, dev.sm_count, stream);
+    a.a = copy, a.sa = scales, rows = a.M;
   }
-  return fp8_impl::launch_wide(a, a.a_rows, dev.sm_count, stream);
+  return wide(a) ? fp8_impl::launch_wide(a, rows, dev.sm_count, stream) : fp8_impl::launch_narrow(a, rows, dev.sm_count, stream);
 }
 
 }  // namespace
@@ -91,11 +90,8 @@ extern "C" int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uin
   return launch(g, nullptr, as_cuda(stream));
 }
 
-extern "C" size_t moe_expert_gemm_workspace(int n_pairs, int E, int K, int in_rows) {
-  moe::GemmArgs g = {};
-  static const int32_t listed = 0;
-  g.offsets = &listed, g.M = n_pairs, g.E = E;
-  if (n_pairs < 1 || E < 1 || K < 16 || in_rows == MOE_ROWS_LIST || !moe::wide(g)) return 0;
+extern "C" size_t moe_expert_gemm_workspace(int n_pairs, int K, int in_rows) {
+  if (n_pairs < 1 || K < 16 || in_rows == MOE_ROWS_LIST) return 0;
   return moe::list_copy_bytes(n_pairs, K);
 }
 
@@ -116,7 +112,7 @@ extern "C" int moe_expert_gemm(const uint8_t* a, const float* a_scales, int64_t 
   if (!offsets || !pairs) return MOE_ERR_INVALID_ARGUMENT;
   if (E > MOE_MAX_EXPERTS) return MOE_ERR_CAPACITY;
   if (!aligned(offsets, 4) || !aligned(pairs, 4) || !aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
-  if (workspace_bytes < moe_expert_gemm_workspace(n_pairs, E, K, in_rows)) return MOE_ERR_WORKSPACE;
-  if (!workspace && moe_expert_gemm_workspace(n_pairs, E, K, in_rows) > 0) return MOE_ERR_WORKSPACE;
+  const size_t need = moe_expert_gemm_workspace(n_pairs, K, in_rows);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
   return launch(g, workspace, as_cuda(stream));
 }

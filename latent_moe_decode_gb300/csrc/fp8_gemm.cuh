@@ -27,11 +27,11 @@ struct GemmArgs {
   uint32_t* err;
 };
 
+// The two kernels. g.a and g.sa hold `rows` rows, grouped in list order (in_rows and
+// a_rows say which rows of the caller's they are, and so which pairs are in range).
 // Few rows per weight tile: weights on the tensor core's 128 lanes, rows on its columns.
-int launch_narrow(const GemmArgs& g, int sm_count, cudaStream_t stream);
-// Many rows per weight tile: rows on the lanes, weights on the columns, two SMs per tile.
-// Grouped, g.a and g.sa hold the rows in list order, `rows` of them (in_rows and a_rows
-// say which rows of the caller's they are, and so which pairs are in range).
+int launch_narrow(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream);
+// Many: rows on the lanes, weights on the columns, two SMs per tile.
 int launch_wide(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream);
 
 // A K-major byte matrix [rows, cols] for TMA: boxes of 128 columns x box_rows rows,
@@ -76,15 +76,17 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 __device__ __forceinline__ int clamp_offset(int v, int n) { return min(max(v, 0), n); }
 
-// The row of a, and of out, of list position i; both -1 (with the error bit) for a pair
-// or a row out of range.
-__device__ __forceinline__ void pair_rows(const GemmArgs& g, int i, long long* in, long long* out) {
-  const int p = __ldg(g.pairs + i);
+// The row of a, and of out, of list position i with pair code p; both -1 (with the error
+// bit) for a pair or a row out of range.
+__device__ __forceinline__ void code_rows(const GemmArgs& g, int i, int p, long long* in, long long* out) {
   const long long r = g.in_rows == MOE_ROWS_TOKEN ? p / g.topk : (g.in_rows == MOE_ROWS_LIST ? i : p);
   const bool ok = p >= 0 && p < g.M && r < g.a_rows;
   if (!ok) set_error(g.err, MOE_DEVERR_ROW_INDEX);
   *in = ok ? r : -1;
   *out = ok ? (g.out_rows == MOE_ROWS_LIST ? i : p) : -1;
+}
+__device__ __forceinline__ void pair_rows(const GemmArgs& g, int i, long long* in, long long* out) {
+  code_rows(g, i, __ldg(g.pairs + i), in, out);
 }
 
 // Exclusive prefix sum of the experts' tile counts, ceil(rows / tile) each, to
