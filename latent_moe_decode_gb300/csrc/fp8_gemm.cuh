@@ -1,6 +1,8 @@
 // Arguments and pieces shared by the tensor-core products of block-128 E4M3 codes.
 #pragma once
 
+#include <atomic>
+
 #include "fp8_block.cuh"
 #include "tcgen05.cuh"
 
@@ -33,6 +35,22 @@ struct GemmArgs {
 int launch_narrow(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream);
 // Many: rows on the lanes, weights on the columns, two SMs per tile.
 int launch_wide(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream);
+
+// A kernel's shared-memory limit and carveout, set at its first launch on a device (two
+// driver calls less on the later ones).
+struct OncePerDevice {
+  std::atomic<uint64_t> done{0};
+  bool allow(const void* kernel, int bytes) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return false;
+    if (done.load(std::memory_order_acquire) >> dev & 1) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        prefer_max_shared(kernel) != MOE_OK)
+      return false;
+    done.fetch_or(1ull << dev, std::memory_order_release);
+    return true;
+  }
+};
 
 // A K-major byte matrix [rows, cols] for TMA: boxes of 128 columns x box_rows rows,
 // 128-byte swizzle, zeros outside.

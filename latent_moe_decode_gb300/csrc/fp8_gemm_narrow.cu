@@ -336,9 +336,8 @@ int launch(const GemmArgs& g, long long a_rows, int S, int stages, size_t smem, 
   if (!make_code_map(&tm_w, g.w, (long long)g.E * g.N, g.K, 128)) return MOE_ERR_CUDA;
   if (!make_code_map(&tm_a, g.a, a_rows, g.K, BN)) return MOE_ERR_CUDA;
   auto kern = narrow_kernel<BN, GROUPED, NG>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - kStaticSmem) != cudaSuccess ||
-      prefer_max_shared(reinterpret_cast<const void*>(kern)) != MOE_OK)
-    return MOE_ERR_CUDA;
+  static OncePerDevice once;
+  if (!once.allow(reinterpret_cast<const void*>(kern), kMaxSmem - kStaticSmem)) return MOE_ERR_CUDA;
   const long long tiles = rows * g.nbn;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : (tiles < sm_count ? tiles : sm_count)));

@@ -344,9 +344,8 @@ int launch(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t strea
   // All the shared memory a CTA may have: the pair holds both SMs' TMEM whole, so nothing
   // that allocates TMEM may share them.
   const size_t smem = kMaxSmem - kStaticSmem;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-      prefer_max_shared(reinterpret_cast<const void*>(kern)) != MOE_OK)
-    return MOE_ERR_CUDA;
+  static OncePerDevice once;
+  if (!once.allow(reinterpret_cast<const void*>(kern), (int)smem)) return MOE_ERR_CUDA;
   const size_t esize = g.f32 ? 4 : 2;
   const int vec = aligned(g.out, 32) && ((size_t)g.N * esize) % 32 == 0;
   const int pairs = sm_count / 2;

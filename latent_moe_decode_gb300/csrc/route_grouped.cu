@@ -1,10 +1,23 @@
 // Routing with softmax or sigmoid scores and groups of experts: scores, balance bias,
 // the groups of largest value, the top-K experts in them, renormalised weights.
 //
-// One warp per token. The token's keys and scores are kept in shared memory; softmax
-// takes the row's maximum and sum by lane strides and shuffle trees; a group's value is
-// found by the warp, the kept groups by topk_group rounds over the groups' values, and
-// the choice by K rounds of a warp argmax over (key descending, expert ascending).
+// A token is 4 E bytes of logits and a few hundred dependent operations, so a call is
+// bound by latency (one token) and by issue (thousands): one warp per token, the row in
+// registers, no step that takes the warp once per choice.
+//   - Keys are FP32 values mapped to integers of the same order (0: not to be chosen), so
+//     that NaN, infinities and dropped experts need no branches.
+//   - Groups: the warp's lanes divide into 32 / n_group lanes per group, scan the keys in
+//     shared memory in a skewed order (no bank conflicts), merge their two largest by
+//     shuffles, and a group is kept when fewer than topk_group order before it.
+//   - Choice: the K-th largest of the 32 lane maxima bounds the K-th largest key from
+//     below (K lanes hold a key at least that large). The experts at or above it, about
+//     K to 2 K, are compacted and ranked against each other by shuffles; more than 64 of
+//     them (heavy ties) take K rounds of a warp argmax instead.
+//   - Softmax without a bias and with groups by their maximum chooses by the logits, the
+//     order of the exact scores; its weights need the row's sum only when they are not
+//     renormalised (e / S over the sum of e / S).
+// More than 1024 experts, or 32 groups, take a plainer body: the row in shared memory,
+// rounds over it for groups and choices.
 #include "topk.cuh"
 
 namespace moe {
@@ -12,6 +25,7 @@ namespace {
 
 using topk_impl::kFull;
 using topk_impl::order_key;
+using topk_impl::rank_key;
 using topk_impl::spec_sigmoid;
 
 constexpr int kWarps = 4;
@@ -23,6 +37,8 @@ struct GroupedArgs {
   int32_t* ids;
   float* weights;
   uint16_t* weights_bf16;
+  int softmax, top2;
+  uint32_t by_size;  // ceil(2^32 / group size): e / size as a high product (groups of two or more)
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -43,8 +59,216 @@ __device__ __forceinline__ float soft_exp(float x, float m) {
   return x == m ? 1.f : expf(x - m);
 }
 
-template <bool SOFTMAX, bool TOP2>
+// The weights of slots 0 .. K - 1 (lane k: slot k's expert and score).
+__device__ __forceinline__ void write_weights(const GroupedArgs& a, int t, int id, float s) {
+  const int lane = threadIdx.x & 31;
+  float S = 0.f;
+  if (a.renorm)
+    for (int k = 0; k < a.K; ++k) S = __fadd_rn(S, __shfl_sync(kFull, s, k));
+  if (lane < a.K) {
+    float w = a.renorm ? (S == 0.f ? 0.f : __fdiv_rn(s, S)) : s;
+    if (a.scale != 1.f) w = __fmul_rn(w, a.scale);
+    const size_t o = (size_t)t * a.K + lane;
+    a.ids[o] = id;
+    if (a.weights) a.weights[o] = w;
+    if (a.weights_bf16) a.weights_bf16[o] = f32_to_bf16(w);
+  }
+}
+
+// Two largest keys of two pairs of them.
+__device__ __forceinline__ void merge2(uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
+  a2 = max(min(a1, b1), max(a2, b2));
+  a1 = max(a1, b1);
+}
+
+constexpr int kMaxE = 1024;  // experts of the register body
+constexpr int kList = 64;    // candidates it ranks
+
+struct RouteScratch {
+  unsigned long long list[kList];  // candidates: (key, ~expert)
+  float x[kList];                  // ... and their logits
+  int id[MOE_MAX_TOPK];            // the choice
+  float s[MOE_MAX_TOPK];
+};
+
+// NJ experts a lane; VEC: expert 128 j + 4 lane + i in element 4 j + i (16-byte loads, no
+// group ends inside one), else expert 32 j + lane in element j. keys: E words of shared
+// memory (GROUPS).
+template <int NJ, bool VEC, bool GROUPS>
+__device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteScratch& ws, uint32_t* keys) {
+  const int lane = threadIdx.x & 31, E = a.E, K = a.K;
+  auto expert = [&](int j) { return VEC ? 128 * (j >> 2) + 4 * lane + (j & 3) : 32 * j + lane; };
+  const float* row = a.logits + (size_t)t * E;
+  float x[NJ];
+  uint32_t key[NJ];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int j = 0; j < NJ; j += 4) {
+      const float4 v = expert(j) < E ? __ldg(reinterpret_cast<const float4*>(row + expert(j))) : make_float4(0, 0, 0, 0);
+      x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) x[j] = expert(j) < E ? __ldg(row + expert(j)) : 0.f;
+  }
+  const bool by_logit = a.softmax && !a.bias && !(GROUPS && a.top2);
+  float m = -INFINITY, inv = 1.f;
+  if (a.softmax) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (expert(j) < E) m = fmaxf(m, x[j]);  // (ignores NaN)
+    m = warp_max(m);
+    if (!by_logit || !a.renorm) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (expert(j) < E) sum = __fadd_rn(sum, soft_exp(x[j], m));
+      sum = warp_sum(sum);
+      inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+    }
+  }
+  auto score = [&](float v) {
+    if (a.softmax) return __fmul_rn(soft_exp(v, m), inv);
+    return v != v ? 0.f : spec_sigmoid(v);
+  };
+  // 1) keys
+  if (by_logit) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) key[j] = expert(j) < E ? order_key(number(x[j])) : 0u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      float c = score(x[j]);
+      if (a.bias && expert(j) < E) c = __fadd_rn(c, __ldg(a.bias + expert(j)));
+      key[j] = expert(j) < E ? order_key(x[j] != x[j] ? -INFINITY : number(c)) : 0u;
+    }
+  }
+  // 2) groups: L lanes each (of a power of two), the two largest keys of a group in each
+  if constexpr (GROUPS) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (expert(j) < E) keys[expert(j)] = key[j];
+    __syncwarp();
+    const int size = E / a.n_group, L = 1 << (31 - __clz(32 / a.n_group)), g = lane / L, r = lane - g * L;
+    const int steps = (size + L - 1) / L;
+    uint32_t k1 = 0, k2 = 0;
+    if (g < a.n_group) {
+      int c = g % steps;  // (each group starts elsewhere: lanes on different banks)
+      for (int i = 0; i < steps; ++i) {
+        const int at = c * L + r;
+        if (at < size) merge2(k1, k2, keys[g * size + at], 0u);
+        if (++c == steps) c = 0;
+      }
+    }
+    for (int o = L >> 1; o > 0; o >>= 1) {
+      const uint32_t o1 = __shfl_xor_sync(kFull, k1, o), o2 = __shfl_xor_sync(kFull, k2, o);
+      merge2(k1, k2, o1, o2);
+    }
+    if (a.top2 && size > 1 && g < a.n_group)
+      k1 = order_key(number(__fadd_rn(topk_impl::key_value(k1), topk_impl::key_value(k2))));
+    int before = 0;  // groups that order before this one
+    for (int o = 0; o < a.n_group; ++o) {
+      const uint32_t ko = __shfl_sync(kFull, k1, o * L);
+      before += ko > k1 || (ko == k1 && o < g);
+    }
+    const uint32_t kept = __ballot_sync(kFull, before < a.topk_group);  // bit g L: group g is kept
+#pragma unroll
+    for (int j = 0; j < NJ; j += VEC ? 4 : 1) {
+      const bool in = kept >> min(__umulhi((uint32_t)expert(j), a.by_size) * (uint32_t)L, 31u) & 1u;  // (past E: whatever)
+#pragma unroll
+      for (int i = 0; i < (VEC ? 4 : 1); ++i)
+        if (!in) key[j + i] = 0u;
+    }
+  }
+  // 3) bound: the K-th largest of the lanes' maxima
+  uint32_t v = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) v = max(v, key[j]);
+  int gt0 = 0, gt1 = 0, ge0 = 0, ge1 = 0;
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const uint32_t o0 = __shfl_sync(kFull, v, i), o1 = __shfl_sync(kFull, v, i + 1);
+    gt0 += o0 > v, ge0 += o0 >= v;
+    gt1 += o1 > v, ge1 += o1 >= v;
+  }
+  const unsigned holds = __ballot_sync(kFull, gt0 + gt1 < K && ge0 + ge1 >= K);
+  const uint32_t bound = max(__shfl_sync(kFull, v, __ffs(holds) - 1), 1u);
+  // 4) candidates, compacted
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) mine += key[j] >= bound;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const int total = __shfl_sync(kFull, incl, 31);
+  if (total <= kList) {
+    int pos = incl - mine;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if (key[j] >= bound) {
+        ws.list[pos] = rank_key(key[j], expert(j));
+        ws.x[pos] = x[j];
+        ++pos;
+      }
+    }
+    __syncwarp();
+    // 5) a candidate's slot: how many order before it
+    const unsigned long long c0 = lane < total ? ws.list[lane] : 0, c1 = lane + 32 < total ? ws.list[lane + 32] : 0;
+    int r0 = 0, r1 = 0;
+#pragma unroll 4
+    for (int i = 0; i < total; ++i) {
+      const unsigned long long o = ws.list[i];
+      r0 += o > c0;
+      r1 += o > c1;
+    }
+    if (lane < total && r0 < K) {
+      ws.id[r0] = (int)(0xFFFFFFFFu - (uint32_t)c0);
+      ws.s[r0] = score(ws.x[lane]);
+    }
+    if (lane + 32 < total && r1 < K) {
+      ws.id[r1] = (int)(0xFFFFFFFFu - (uint32_t)c1);
+      ws.s[r1] = score(ws.x[lane + 32]);
+    }
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+      uint32_t best = 0;
+      int at = 0x7FFFFFFF;
+      float bx = 0.f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (key[j] > best) best = key[j], at = expert(j), bx = x[j];  // (ascending: the first maximum wins)
+      const uint32_t top = __reduce_max_sync(kFull, best);
+      const int win = (int)__reduce_min_sync(kFull, best == top ? (uint32_t)at : 0x7FFFFFFFu);
+      if (at == win) {
+        ws.id[k] = win;
+        ws.s[k] = score(bx);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (expert(j) == win) key[j] = 0u;
+    }
+  }
+  __syncwarp();
+  write_weights(a, t, lane < K ? ws.id[lane] : 0, lane < K ? ws.s[lane] : 0.f);
+}
+
+template <int NJ, bool VEC, bool GROUPS>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(const GroupedArgs a) {
+  __shared__ RouteScratch ws[kWarps];
+  __shared__ uint32_t keys[GROUPS ? kWarps * NJ * 32 : 1];
+  const int warp = threadIdx.x >> 5, t = blockIdx.x * kWarps + warp;
+  grid_launch_dependents();
+  if (t < a.T && (threadIdx.x & 31) == 0 && VEC) prefetch_l2(a.logits + (size_t)t * a.E, (uint32_t)a.E * 4u);  // (a hint)
+  grid_wait();
+  if (t < a.T) route_token<NJ, VEC, GROUPS>(a, t, ws[warp], keys + (GROUPS ? warp * NJ * 32 : 0));
+}
+
+template <bool SOFTMAX, bool TOP2>
+__global__ void __launch_bounds__(32 * kWarps) route_any_kernel(const GroupedArgs a) {
   extern __shared__ float smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float* key = smem + (size_t)warp * (2 * a.E + MOE_MAX_GROUPS);
@@ -121,16 +345,23 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const GroupedArgs a)
     if (lane == 0) key[win] = __uint_as_float(0x7FC00000u);
     __syncwarp();
   }
-  float S = 0.f;
-  for (int k = 0; k < a.K; ++k) S = __fadd_rn(S, __shfl_sync(kFull, my_s, k));
-  if (lane < a.K) {
-    float w = a.renorm ? (S == 0.f ? 0.f : __fdiv_rn(my_s, S)) : my_s;
-    if (a.scale != 1.f) w = __fmul_rn(w, a.scale);
-    const size_t o = (size_t)t * a.K + lane;
-    a.ids[o] = my_id;
-    if (a.weights) a.weights[o] = w;
-    if (a.weights_bf16) a.weights_bf16[o] = f32_to_bf16(w);
-  }
+  write_weights(a, t, my_id, my_s);
+}
+
+template <int NJ, bool VEC>
+int launch_registers(const GroupedArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)((a.T + kWarps - 1) / kWarps)), block(32 * kWarps);
+  if (a.n_group > 1 && a.topk_group < a.n_group) return launch_pdl(route_kernel<NJ, VEC, true>, grid, block, 0, s, a);
+  return launch_pdl(route_kernel<NJ, VEC, false>, grid, block, 0, s, a);
+}
+
+template <bool VEC>
+int launch_nj(const GroupedArgs& a, cudaStream_t s) {
+  if (a.E <= 128) return launch_registers<4, VEC>(a, s);
+  if (a.E <= 256) return launch_registers<8, VEC>(a, s);
+  if (a.E <= 512) return launch_registers<16, VEC>(a, s);
+  if (a.E <= 896) return launch_registers<28, VEC>(a, s);
+  return launch_registers<32, VEC>(a, s);
 }
 
 }  // namespace
@@ -153,11 +384,18 @@ extern "C" int moe_topk_route_grouped(const float* logits, const float* bias, in
   DeviceInfo dev;
   int st = current_device(&dev);
   if (st != MOE_OK) return st;
-  const GroupedArgs a{logits, bias, T, E, K, n_group, topk_group, renormalize, scale, ids, weights, weights_bf16};
-  const int warps = E <= 1024 ? kWarps : 1;
+  const int size = E / n_group;
+  GroupedArgs a{logits, bias, T, E, K, n_group, topk_group, renormalize, scale, ids, weights, weights_bf16};
+  a.softmax = scoring == MOE_SCORE_SOFTMAX, a.top2 = group_rule == MOE_GROUP_TOP2;
+  a.by_size = size > 1 ? (uint32_t)(((1ull << 32) + size - 1) / size) : 0;
+  const bool grouped = n_group > 1 && topk_group < n_group;
+  if (E <= kMaxE && (!grouped || (n_group <= 32 && size > 1))) {
+    const bool vec = E % 4 == 0 && aligned(logits, 16) && (!grouped || size % 4 == 0);
+    return vec ? launch_nj<true>(a, as_cuda(stream)) : launch_nj<false>(a, as_cuda(stream));
+  }
+  const int warps = E <= kMaxE ? kWarps : 1;
   const size_t smem = (size_t)warps * (2 * E + MOE_MAX_GROUPS) * sizeof(float);  // at most 34 KB
-  const bool soft = scoring == MOE_SCORE_SOFTMAX, two = group_rule == MOE_GROUP_TOP2;
-  auto kern = soft ? (two ? route_kernel<true, true> : route_kernel<true, false>)
-                   : (two ? route_kernel<false, true> : route_kernel<false, false>);
+  auto kern = a.softmax ? (a.top2 ? route_any_kernel<true, true> : route_any_kernel<true, false>)
+                        : (a.top2 ? route_any_kernel<false, true> : route_any_kernel<false, false>);
   return launch_pdl(kern, dim3((T + warps - 1) / warps), dim3(32 * warps), smem, as_cuda(stream), a);
 }
