@@ -18,8 +18,26 @@ int check(const GemmArgs& a, int out_dtype) {
   return MOE_OK;
 }
 
-// Which kernel. Measured (N = 7168, K = 3584) ...
-bool wide(const GemmArgs& a) { return a.offsets ? (long long)a.M >= 96LL * a.E : a.M >= 256; }
+// Which kernel. Grouped: by the lists' average length (a tile of 256 rows wastes less than
+// it gains from there on).
+// Dense: up to 64 rows, weights on the lanes; above, whichever is estimated to end first.
+// A wide pair spends 0.43 us on a block of a tile and about 4 us on the rest; a CTA of the
+// other form 0.35 us on a block of 64 rows when it has an SM to itself, 0.4 a CTA when two
+// share one, and 3.5 on the rest. (Splitting K over pairs of a wide tile, too, measured
+// slower than either: 15 us for 128 x 7168 x 3584 against 14.9 unsplit, 29 for 333 x 2016 x
+// 7184 against 18.8, the sum of 128 KB of partials a CTA and clusters of four or eight
+// whole SMs costing more than the blocks saved.)
+bool wide(const GemmArgs& a, int sm_count) {
+  if (a.offsets) return (long long)a.M >= 96LL * a.E;
+  if (a.M <= 64) return false;
+  const long long wide_tiles = (((long long)a.M - 1) / 256 + 1) * ((a.nbn + 1) / 2), pairs = sm_count / 2;
+  const long long wide_ns = 4000 + ((wide_tiles - 1) / pairs + 1) * a.nbk * 430;
+  const long long tiles = (((long long)a.M - 1) / 64 + 1) * a.nbn;
+  const int n = fp8_impl::narrow_splits(tiles, a.nbk, sm_count);
+  const long long waves = (tiles * n - 1) / sm_count + 1;
+  const long long narrow_ns = 3500 + waves * ((a.nbk - 1) / n + 1) * (n > 1 ? 400 : 350);
+  return wide_ns < narrow_ns;
+}
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -73,7 +91,7 @@ int launch(GemmArgs& a, void* workspace, cudaStream_t stream) {
     if (st != MOE_OK) return st;
     a.a = copy, a.sa = scales, rows = a.M;
   }
-  return wide(a) ? fp8_impl::launch_wide(a, rows, dev.sm_count, stream) : fp8_impl::launch_narrow(a, rows, dev.sm_count, stream);
+  return wide(a, dev.sm_count) ? fp8_impl::launch_wide(a, rows, dev.sm_count, stream) : fp8_impl::launch_narrow(a, rows, dev.sm_count, stream);
 }
 
 }  // namespace

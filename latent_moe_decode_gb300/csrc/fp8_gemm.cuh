@@ -11,7 +11,7 @@ namespace fp8_impl {
 
 constexpr int kMaxSmem = 227 * 1024;  // shared memory a CTA may have
 constexpr int kSmSmem = 228 * 1024;   // ... and an SM, 1 KB of it reserved per CTA
-constexpr int kStaticSmem = 2048;     // an upper bound on the kernels' static shared memory and the reserve
+constexpr int kStaticSmem = 1536;     // an upper bound on a kernel's static shared memory and its reserve
 constexpr int kMaxRowTiles = 1 << 30;
 
 struct GemmArgs {
@@ -35,6 +35,8 @@ struct GemmArgs {
 int launch_narrow(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream);
 // Many: rows on the lanes, weights on the columns, two SMs per tile.
 int launch_wide(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream);
+// CTAs that a dense narrow product of `tiles` tiles puts to work on each.
+int narrow_splits(long long tiles, int nbk, int sm_count);
 
 // A kernel's shared-memory limit and carveout, set at its first launch on a device (two
 // driver calls less on the later ones).

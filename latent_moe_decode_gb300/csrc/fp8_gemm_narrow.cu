@@ -7,9 +7,9 @@
 // scale, one 128-byte swizzle row, and four K = 32 MMAs. Each stage's sum goes to its own
 // TMEM slot (the accumulator starts anew), and the epilogue warps fold it into FP32
 // registers with the block's scales while the next stages multiply:
-//   - NG groups of four epilogue warps, one weight row (TMEM lane) per thread and BN
-//     accumulators each; with two groups they take the tiles in turn, each with TMEM
-//     slots of its own, so one tile's output and the next tile's first blocks overlap;
+//   - NG groups of 4 CG epilogue warps, one weight row (TMEM lane) and BN / CG columns per
+//     thread; with two groups they take the tiles in turn, each with TMEM slots of its
+//     own, so one tile's output and the next tile's first blocks overlap;
 //   - a TMA producer warp (a box of weights and one of rows a stage) and an MMA issuer warp;
 //   - a scale warp: the columns' scales of a block, times the weights' scale, to shared
 //     memory beside the block's TMEM slot (one barrier tells the epilogue of both).
@@ -30,12 +30,12 @@ constexpr int kWBytes = 128 * FP8_BLOCK;  // the weights of a stage
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplits = 8;
 
-template <int BN, int NG>
+template <int BN, int NG, int CG>
 struct Narrow {
-  static constexpr int kEpiWarps = 4 * NG;
+  static constexpr int kEpiWarps = 4 * NG * CG;
   static constexpr int kThreads = 32 * (kEpiWarps + 3);
   static constexpr int kStageBytes = kWBytes + BN * FP8_BLOCK;
-  static constexpr int kSlots = BN <= 32 ? 4 : 2;    // TMEM accumulators of a group
+  static constexpr int kSlots = BN <= 32 || NG == 1 ? 4 : 2;  // TMEM accumulators of a group
   static constexpr int kTmemCols = NG * kSlots * BN;  // 64 .. 256
   static constexpr int kScaleBytes = NG * kSlots * BN * 4;
 };
@@ -73,11 +73,11 @@ __device__ __forceinline__ void store(const GemmArgs& g, long long row, int n, f
     static_cast<uint16_t*>(g.out)[row * g.N + n] = f32_to_bf16(v);
 }
 
-template <int BN, bool GROUPED, int NG>
-__global__ void __launch_bounds__(Narrow<BN, NG>::kThreads)
+template <int BN, bool GROUPED, int NG, int CG>
+__global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, NG == 1 ? 2 : 1)
     narrow_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const GemmArgs g,
                   long long a_rows, int stages, int S, int max_row_tiles) {
-  using C = Narrow<BN, NG>;
+  using C = Narrow<BN, NG, CG>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 3 * NG * C::kSlots];
   __shared__ uint32_t tmem_slot;
@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(Narrow<BN, NG>::kThreads)
     }
     for (int i = 0; i < NG * C::kSlots; ++i) {
       mbar_init(tfull(i), 2);   // the MMA's commit and the scale warp
-      mbar_init(tempty(i), 4);  // one arrival per epilogue warp of the group
-      mbar_init(sempty(i), 4);
+      mbar_init(tempty(i), 4 * CG);  // one arrival per epilogue warp of the group
+      mbar_init(sempty(i), 4 * CG);
     }
     mbar_fence_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
@@ -224,10 +224,12 @@ __global__ void __launch_bounds__(Narrow<BN, NG>::kThreads)
       if (NG == 2) grp ^= 1;
     }
   } else {  // epilogue
-    constexpr int CL = (BN + 31) / 32;
-    constexpr int P = BN < 32 ? BN : 32;  // columns per TMEM load
-    const int grp = warp >> 2, row = threadIdx.x & 127;  // its group, its weight row of a tile
-    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    constexpr int CW = BN / CG;           // columns of a thread
+    constexpr int CL = (CW + 31) / 32;
+    constexpr int P = CW < 32 ? CW : 32;  // columns per TMEM load
+    const int grp = (warp >> 2) / CG, c0 = (warp >> 2) % CG * CW;  // its group, its first column
+    const int row = threadIdx.x & 127;                             // its weight row of a tile
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
     uint32_t i = 0;
     bool ok = true;
     for (int t = t0 + grp * step; t < tiles && ok; t += NG * step) {
@@ -235,18 +237,18 @@ __global__ void __launch_bounds__(Narrow<BN, NG>::kThreads)
       int code[CL];  // (used only at the tile's end)
 #pragma unroll
       for (int j = 0; j < CL; ++j)
-        code[j] = GROUPED && lane + 32 * j < ti.cnt ? __ldg(g.pairs + ti.pos + lane + 32 * j) : 0;
-      float acc[BN];
+        code[j] = GROUPED && c0 + lane + 32 * j < ti.cnt ? __ldg(g.pairs + ti.pos + c0 + lane + 32 * j) : 0;
+      float acc[CW];
 #pragma unroll
-      for (int j = 0; j < BN; ++j) acc[j] = 0.f;
+      for (int j = 0; j < CW; ++j) acc[j] = 0.f;
       for (int kb = kb0; kb < kb1; ++kb, ++i) {
         const int sl = grp * C::kSlots + (int)(i & kMask);
         ok = __all_sync(kFullMask, mbar_wait_asleep(tfull(sl), lap(i), g.err));
         if (!ok) break;
         tcgen05_after_sync();
-        const float4* const sc = reinterpret_cast<const float4*>(scale_mem + sl * BN);
+        const float4* const sc = reinterpret_cast<const float4*>(scale_mem + sl * BN + c0);
 #pragma unroll
-        for (int p = 0; p < BN / P; ++p) {
+        for (int p = 0; p < CW / P; ++p) {
           uint32_t v[P];
           if constexpr (P == 16)
             tmem_ld16(tl + sl * BN, v);
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(Narrow<BN, NG>::kThreads)
             tmem_ld32(tl + sl * BN + p * P, v);
           tmem_wait_ld();
           tmem_loaded(v);
-          if (p == BN / P - 1) {  // the sums are read
+          if (p == CW / P - 1) {  // the sums are read
             tcgen05_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty(sl));
@@ -278,9 +280,9 @@ __global__ void __launch_bounds__(Narrow<BN, NG>::kThreads)
         long long out_row[CL];
 #pragma unroll
         for (int j = 0; j < CL; ++j) {
-          const int c = lane + 32 * j;
+          const int c = c0 + lane + 32 * j;
           long long in, out = -1;
-          if (c < ti.cnt) {
+          if (c < ti.cnt && lane + 32 * j < CW) {
             if constexpr (GROUPED)
               code_rows(g, ti.pos + c, code[j], &in, &out);
             else
@@ -289,27 +291,27 @@ __global__ void __launch_bounds__(Narrow<BN, NG>::kThreads)
           out_row[j] = out;
         }
 #pragma unroll
-        for (int c = 0; c < BN; ++c) {
+        for (int c = 0; c < CW; ++c) {
           const long long r = __shfl_sync(kFullMask, out_row[c / 32], c & 31);
           if (r >= 0 && n < g.N) store(g, r, n, acc[c]);
         }
       } else {  // partial columns for the cluster's sum (the stages are all consumed)
         float* part = reinterpret_cast<float*>(mem);
 #pragma unroll
-        for (int c = 0; c < BN; ++c) part[c * 128 + row] = acc[c];
+        for (int c = 0; c < CW; ++c) part[(c0 + c) * 128 + row] = acc[c];
       }
     }
   }
   if (S > 1) {  // (one tile per cluster; dense)
     __syncwarp();
     cluster_sync();  // every split's partial is written and visible
-    if (warp < 4) {
+    if (warp < C::kEpiWarps) {
       const Tile ti = tile_at<BN, GROUPED>(g, table, t0);
-      const int n = ti.n0 + threadIdx.x;
+      const int row = threadIdx.x & 127, n = ti.n0 + row;
       uint32_t peer[kMaxSplits];
 #pragma unroll
-      for (int q = 0; q < kMaxSplits; ++q) peer[q] = map_rank(base, q < S ? q : 0) + 4u * threadIdx.x;
-      for (int c = rank; c < ti.cnt; c += S) {
+      for (int q = 0; q < kMaxSplits; ++q) peer[q] = map_rank(base, q < S ? q : 0) + 4u * row;
+      for (int c = rank + S * (warp >> 2); c < ti.cnt; c += S * NG * CG) {
         float sum = 0.f;
 #pragma unroll
         for (int q = 0; q < kMaxSplits; ++q) {
@@ -330,18 +332,18 @@ __global__ void __launch_bounds__(Narrow<BN, NG>::kThreads)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
 }
 
-template <int BN, bool GROUPED, int NG>
+template <int BN, bool GROUPED, int NG, int CG>
 int launch(const GemmArgs& g, long long a_rows, int S, int stages, size_t smem, long long rows, int sm_count, cudaStream_t stream) {
   CUtensorMap tm_w, tm_a;
   if (!make_code_map(&tm_w, g.w, (long long)g.E * g.N, g.K, 128)) return MOE_ERR_CUDA;
   if (!make_code_map(&tm_a, g.a, a_rows, g.K, BN)) return MOE_ERR_CUDA;
-  auto kern = narrow_kernel<BN, GROUPED, NG>;
+  auto kern = narrow_kernel<BN, GROUPED, NG, CG>;
   static OncePerDevice once;
   if (!once.allow(reinterpret_cast<const void*>(kern), kMaxSmem - kStaticSmem)) return MOE_ERR_CUDA;
   const long long tiles = rows * g.nbn;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : (tiles < sm_count ? tiles : sm_count)));
-  cfg.blockDim = dim3(Narrow<BN, NG>::kThreads);
+  cfg.blockDim = dim3(Narrow<BN, NG, CG>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -356,9 +358,10 @@ int launch(const GemmArgs& g, long long a_rows, int S, int stages, size_t smem, 
 
 template <int BN, bool GROUPED>
 int plan(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t stream) {
-  constexpr int kGroups = BN <= 64 ? 2 : 1;  // (of 128 columns one group's registers and TMEM are enough)
-  using One = Narrow<BN, 1>;
-  using Many = Narrow<BN, kGroups>;
+  constexpr int kGroups = 2;
+  constexpr int kHalves = BN == 64 ? 2 : 1;  // (64 accumulators a thread would leave room for one CTA an SM)
+  using One = Narrow<BN, 1, kHalves>;
+  using Many = Narrow<BN, kGroups, 1>;
   // row tiles (grouped: at most, of ascending offsets)
   const long long rows = GROUPED ? (long long)g.M / BN + (g.E < g.M ? g.E : g.M) : ((long long)g.M + BN - 1) / BN;
   const long long tiles = rows * g.nbn;
@@ -367,24 +370,27 @@ int plan(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t stream)
   // an SM holds never ask for more than its 512 columns: tcgen05.alloc would make one
   // wait for another, in a ring of waits where clusters meet at barriers.
   auto shared = [&](size_t extra, int stages, int stage_bytes, int cols) {
-    const size_t need = 1024 + extra + (size_t)stages * stage_bytes, least = (size_t)cols * (kSmSmem / 512);
+    const size_t need = 1024 + extra + (size_t)stages * stage_bytes, least = (size_t)cols * (kSmSmem / 512) - kStaticSmem;
     return need < least ? least : need;
   };
   if constexpr (!GROUPED) {
-    // the most splits whose CTAs are all resident at once, two per SM while they fit
-    for (int s = kMaxSplits; s >= 2; --s) {
-      const int kbs = (g.nbk + s - 1) / s, st = kbs < kMaxStages ? kbs : kMaxStages;
-      const size_t bytes = shared(One::kScaleBytes, st, One::kStageBytes, One::kTmemCols) + kStaticSmem;
-      const int per_sm = 2 * bytes <= (size_t)kSmSmem ? 2 : 1;
-      if (s <= g.nbk && bytes <= (size_t)kMaxSmem && (size_t)st * One::kStageBytes >= (size_t)BN * 512 &&
-          tiles * s <= (long long)per_sm * sm_count)
-        return launch<BN, false, 1>(g, a_rows, s, st, bytes - kStaticSmem, rows, sm_count, stream);
+    // Split K while there are SMs without work: into the most parts whose CTAs are resident
+    // at once, two per SM (a part's blocks need not all have a stage).
+    constexpr int kMost = (kSmSmem / 2 - kStaticSmem - 1024 - One::kScaleBytes) / One::kStageBytes;
+    static_assert((size_t)kMost * One::kStageBytes >= (size_t)BN * 512, "the stages hold a partial tile");
+    const int s = narrow_splits(tiles, g.nbk, sm_count);
+    if (s > 1) {
+      const int kbs = (g.nbk + s - 1) / s;
+      int st = kbs < kMost ? kbs : kMost;
+      while ((size_t)st * One::kStageBytes < (size_t)BN * 512) ++st;
+      return launch<BN, false, 1, kHalves>(g, a_rows, s, st, shared(One::kScaleBytes, st, One::kStageBytes, One::kTmemCols), rows,
+                                  sm_count, stream);
     }
   }
   const size_t extra = Many::kScaleBytes + (GROUPED ? 2 * (g.E + 1) * 4 : 0);
   int stages = (int)((kMaxSmem - kStaticSmem - 1024 - extra) / Many::kStageBytes);
   if (stages > kMaxStages) stages = kMaxStages;
-  return launch<BN, GROUPED, kGroups>(g, a_rows, 1, stages, shared(extra, stages, Many::kStageBytes, Many::kTmemCols), rows,
+  return launch<BN, GROUPED, kGroups, 1>(g, a_rows, 1, stages, shared(extra, stages, Many::kStageBytes, Many::kTmemCols), rows,
                                       sm_count, stream);
 }
 
@@ -393,18 +399,23 @@ int launch_bn(int bn, const GemmArgs& g, long long a_rows, int sm_count, cudaStr
   switch (bn) {
     case 16: return plan<16, GROUPED>(g, a_rows, sm_count, stream);
     case 32: return plan<32, GROUPED>(g, a_rows, sm_count, stream);
-    case 64: return plan<64, GROUPED>(g, a_rows, sm_count, stream);
-    default: return plan<128, GROUPED>(g, a_rows, sm_count, stream);
+    default: return plan<64, GROUPED>(g, a_rows, sm_count, stream);
   }
 }
 
 }  // namespace
 
+int narrow_splits(long long tiles, int nbk, int sm_count) {
+  for (int s = kMaxSplits; s >= 2; --s)
+    if (s <= nbk && tiles * s <= 2LL * sm_count) return s;
+  return 1;
+}
+
 int launch_narrow(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream) {
   // dense: the narrowest tile that holds every row; grouped: that holds an expert of average load and half
   const long long want = g.offsets ? (3LL * g.M / 2 + g.E - 1) / g.E : g.M;
   int bn = 16;
-  while (bn < 128 && bn < want) bn *= 2;
+  while (bn < 64 && bn < want) bn *= 2;
   return g.offsets ? launch_bn<true>(bn, g, rows, sm_count, stream) : launch_bn<false>(bn, g, rows, sm_count, stream);
 }
 
