@@ -21,7 +21,9 @@ namespace {
 
 using namespace fp8_impl;
 
-constexpr int kMaxThreads = 512;
+// Threads of a CTA: one fragment each up to H = 8192, else four (more registers a thread).
+template <int V>
+constexpr int kMaxThreads = V == 1 ? 1024 : 512;
 constexpr int kMaxH = 16384;
 
 constexpr int kMaxStages = 4;
@@ -31,7 +33,7 @@ struct BlockNormArgs {
   long long ldy;
   const void* residual;
   const uint16_t *post, *gate, *next;
-  float alpha, eps;
+  float alpha, eps, inv_h;  // inv_h: 1 / H
   int T, H, nb;
   int stages;  // of the ring (streamed)
   uint32_t* err;
@@ -41,21 +43,26 @@ struct BlockNormArgs {
   float* scales;
 };
 
-// The CTA's sum of one value per thread, in a fixed order, for every thread.
-__device__ __forceinline__ float cta_sum(float v, float* slots) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFullMask, v, o));
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  return v;
+}
+
+// The CTA's sum of one value per thread, in a fixed order, for every thread: trees over a
+// warp's lanes, then (in every warp) over the warps' sums.
+__device__ __forceinline__ float cta_sum(float v, float* slots) {
+  const int lane = threadIdx.x & 31;
+  v = warp_sum(v);
+  if (lane == 0) slots[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s = __fadd_rn(s, slots[w]);
-  return s;
+  return warp_sum(lane < (int)(blockDim.x >> 5) ? slots[lane] : 0.f);
 }
 
 template <int V, bool F32, int GATE, bool STREAM>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads<V>) block_norm_kernel(const BlockNormArgs a) {
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float slots[2][kMaxThreads / 32];
+  __shared__ float slots[2][kMaxThreads<V> / 32];
   __shared__ __align__(8) uint64_t bars[kMaxStages];
   const int nv = a.H / 8;  // fragments of a row
   // a stage: the row of y, of the residual, of a full gate
@@ -132,7 +139,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
       for (int j = 0; j < 8; ++j) ss = __fmaf_rn(y[i][j], y[i][j], ss);
     float root = 1.f;
     if (a.post)
-      root = __frsqrt_rn(__fadd_rn(__fdiv_rn(cta_sum(ss, slots[0]), (float)a.H), a.eps));
+      root = rsqrtf(__fmaf_rn(cta_sum(ss, slots[0]), a.inv_h, a.eps));
     else if (STREAM)
       __syncthreads();
     if (STREAM) {  // every thread has its fragments: the stage takes the row after the ring's
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
         }
       }
     }
-    root = __frsqrt_rn(__fadd_rn(__fdiv_rn(cta_sum(ss, slots[1]), (float)a.H), a.eps));
+    root = rsqrtf(__fmaf_rn(cta_sum(ss, slots[1]), a.inv_h, a.eps));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int f = i * blockDim.x + threadIdx.x;
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
 #pragma unroll
           for (int j = 0; j < 8; ++j) w[j] = 0.f;
         }
-        const BlockScale s = block_scale<false>(block_max(magnitude(w)));
+        const BlockScale s = block_scale_shared(block_max(magnitude(w)));
         if (f < nv) {
           *reinterpret_cast<uint2*>(a.q + at + 8 * f) = encode8(w, s);
           if ((f & 15) == 0) a.scales[row * a.nb + (f >> 4)] = s.scale;
@@ -247,14 +254,13 @@ extern "C" int moe_block_norm(const uint16_t* y, int64_t ldy, const void* residu
   if (st != MOE_OK) return st;
   BlockNormArgs a;
   a.y = y, a.ldy = ldy, a.residual = residual, a.post = post_weight, a.gate = gate, a.next = next_weight;
-  a.alpha = alpha, a.eps = eps, a.T = T, a.H = H, a.nb = (H + FP8_BLOCK - 1) / FP8_BLOCK;
+  a.alpha = alpha, a.eps = eps, a.inv_h = 1.f / (float)H, a.T = T, a.H = H, a.nb = (H + FP8_BLOCK - 1) / FP8_BLOCK;
   a.h = h, a.n = n, a.q = q, a.scales = scales, a.err = dev.error_word;
-  const int nv = H / 8, v = nv <= kMaxThreads ? 1 : (nv <= 2 * kMaxThreads ? 2 : 4);
+  const int nv = H / 8, v = nv <= kMaxThreads<1> ? 1 : 4;
   const int threads = ((nv + v - 1) / v + 31) / 32 * 32;
   const cudaStream_t s = as_cuda(stream);
   const bool f32 = residual_dtype == MOE_DTYPE_F32;
   const int sms = dev.sm_count;
   if (v == 1) return f32 ? launch_gate<1, true>(gate_kind, a, threads, sms, s) : launch_gate<1, false>(gate_kind, a, threads, sms, s);
-  if (v == 2) return f32 ? launch_gate<2, true>(gate_kind, a, threads, sms, s) : launch_gate<2, false>(gate_kind, a, threads, sms, s);
   return f32 ? launch_gate<4, true>(gate_kind, a, threads, sms, s) : launch_gate<4, false>(gate_kind, a, threads, sms, s);
 }

@@ -45,11 +45,25 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t m) {
   return s;
 }
 
+// The same (amax / 448) with the warp's lanes in step and a block's lanes agreeing on m:
+// even lanes divide for the scale, odd lanes for the multiplier.
+__device__ __forceinline__ BlockScale block_scale_shared(uint32_t m) {
+  BlockScale s;
+  s.special = m >= kInf;
+  const float amax = __uint_as_float(min(max(m, kTiny), kInf - 1u));
+  const bool odd = threadIdx.x & 1;
+  const float d = __fdiv_rn(odd ? 448.f : amax, odd ? amax : 448.f), o = __shfl_xor_sync(kFullMask, d, 1);
+  s.scale = s.special ? __uint_as_float(0x7FC00000u) : m == 0u ? 1.f : odd ? o : d;
+  s.mult = m == 0u ? 1.f : odd ? d : o;
+  return s;
+}
+
+// Bits of the largest magnitude of 8 values, NaN above all.
 __device__ __forceinline__ uint32_t magnitude(const float (&v)[8]) {
-  uint32_t m = 0;
+  float m = fabsf(v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return m;
+  for (int i = 1; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[i])));
+  return __float_as_uint(m);
 }
 
 // The largest magnitude over the 16 lanes of a block.

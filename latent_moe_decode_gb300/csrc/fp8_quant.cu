@@ -32,14 +32,6 @@ __device__ __forceinline__ float silu(float g) {
   return __fmul_rn(g, r);
 }
 
-// The largest magnitude of 8 values, NaN above all.
-__device__ __forceinline__ float largest(const float (&v)[8]) {
-  float m = fabsf(v[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[i])));
-  return m;
-}
-
 // units: rows times the runs of a row.
 template <bool SWIGLU, bool POW2>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __restrict__ x, long long ldx, int cols,
@@ -70,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __re
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(silu(v[i][j]), up[j]);
       }
-      m[i] = __float_as_uint(largest(v[i]));  // (magnitudes and NaN: the integer order is theirs)
+      m[i] = magnitude(v[i]);
     }
     // lanes with bits 3, 2 = i end with the maximum of load i's block
     static_assert(kUnroll == 4, "two exchange steps");
