@@ -83,40 +83,63 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// 64 outputs of one row from column n on: whole 32-byte sectors a store where the rows
-// are so aligned and the columns all exist (vec), else one by one.
-__device__ __forceinline__ void store_row(const GemmArgs& g, long long row, int n, const float (&acc)[64], bool vec) {
-  if (g.f32) {
-    float* o = static_cast<float*>(g.out) + row * g.N + n;
+// Four lanes' four 32-byte pieces, transposed: lane j of the four ends with piece j of each.
+__device__ __forceinline__ void transpose4(uint32_t (&u)[4][8]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t v[8];
+  for (int step = 1; step <= 2; step <<= 1) {
+    const bool up = lane & step;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(acc[8 * i + j]);
-      if (vec) {
-        st32(o + 8 * i, v);
-      } else {
+    for (int a = 0; a < 4; ++a) {
+      if (a & step) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (n + 8 * i + j < g.N) o[8 * i + j] = __uint_as_float(v[j]);
+      for (int w = 0; w < 8; ++w) {
+        const uint32_t got = __shfl_xor_sync(kFullMask, up ? u[a][w] : u[a + step][w], step);
+        (up ? u[a][w] : u[a + step][w]) = got;
       }
     }
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(g.out) + row * g.N + n;
+  }
+}
+
+// The warp's 64 columns from n on of its 32 rows (`row` this lane's, -1: none). With whole,
+// 32-byte aligned pieces (vec) four lanes exchange theirs first, so that a store covers 128
+// contiguous bytes of eight rows and not 32 of all 32 (those took an eighth of the time of
+// 4096 x 7168 x 3584); else one by one.
+__device__ __forceinline__ void store_rows(const GemmArgs& g, long long row, int n, const float (&acc)[64], bool vec) {
+  const int lane = threadIdx.x & 31;
+  if (vec) {
+    uint32_t u[4][8];
+    auto store4 = [&](int size, int at) {  // bytes a value; first column
+      transpose4(u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(acc[16 * i + 2 * j], acc[16 * i + 2 * j + 1]);
-      if (vec) {
-        st32(o + 16 * i, v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (n + 16 * i + 2 * j < g.N) o[16 * i + 2 * j] = (uint16_t)v[j];
-          if (n + 16 * i + 2 * j + 1 < g.N) o[16 * i + 2 * j + 1] = (uint16_t)(v[j] >> 16);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const long long r = __shfl_sync(kFullMask, row, (lane & ~3) + i);
+        if (r >= 0) st32(static_cast<uint8_t*>(g.out) + (r * g.N + at) * size + 32 * (lane & 3), u[i]);
       }
+    };
+    if (g.f32) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i >> 3][i & 7] = __float_as_uint(acc[32 * half + i]);
+        store4(4, n + 32 * half);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) u[i >> 3][i & 7] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
+      store4(2, n);
+    }
+  } else if (row >= 0) {
+    if (g.f32) {
+      float* o = static_cast<float*>(g.out) + row * g.N + n;
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        if (n + i < g.N) o[i] = acc[i];
+    } else {
+      uint16_t* o = static_cast<uint16_t*>(g.out) + row * g.N + n;
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        if (n + i < g.N) o[i] = f32_to_bf16(acc[i]);
     }
   }
 }
@@ -315,12 +338,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
       if (!ok) break;
       const Tile ti = tile_at<GROUPED>(g, table, t, half);
+      long long in, out = -1;
       if (row < ti.cnt) {
-        long long in, out = ti.pos + row;
+        out = ti.pos + row;
         if constexpr (GROUPED) pair_rows(g, ti.pos + row, &in, &out);
-        const int n = ti.n0 + cg * 64;
-        if (out >= 0 && n < g.N) store_row(g, out, n, acc, vec && n + 64 <= g.N);
       }
+      const int n = ti.n0 + cg * 64;
+      __syncwarp();
+      if (n < g.N) store_rows(g, out, n, acc, vec && n + 64 <= g.N);
       __syncwarp();
     }
   }
