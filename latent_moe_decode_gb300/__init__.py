@@ -119,17 +119,20 @@ def _ptr(t):
 
 
 def _need(t, dtype, shape=None, name="tensor"):
+    try:  # (a torch.Size compares as the tuple that it is)
+        if t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous() and t.is_cuda:
+            return t
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dtype is not dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if shape is not None and t.shape != shape:  # (a torch.Size compares as the tuple that it is)
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _empty(shape, dtype, like):
@@ -523,19 +526,20 @@ def block_norm(y, residual, next_weight, post_weight=None, gate=None, alpha: flo
     scales (else None). gate: BF16 [T, 1], [H] or [T, H]. h may be the residual itself."""
     T, H = residual.shape
     _rows_2d(y, torch.bfloat16, "y")
-    if tuple(y.shape) != (T, H):
+    if y.shape != (T, H):
         raise ValueError(f"y: expected shape {(T, H)}, got {tuple(y.shape)}")
     dt, code = _out_dtype(residual, None)
-    _need(residual, dt, (T, H), "residual")
-    _need(next_weight, torch.bfloat16, (H,), "next_weight")
+    full, row = (T, H), (H,)
+    _need(residual, dt, full, "residual")
+    _need(next_weight, torch.bfloat16, row, "next_weight")
     if post_weight is not None:
-        _need(post_weight, torch.bfloat16, (H,), "post_weight")
+        _need(post_weight, torch.bfloat16, row, "post_weight")
     kind = GATE_NONE
     if gate is not None:
         _need(gate, torch.bfloat16, None, "gate")
-        kind = {(T, H): GATE_FULL, (H,): GATE_CHANNEL, (T, 1): GATE_TOKEN}.get(tuple(gate.shape))
+        kind = {full: GATE_FULL, row: GATE_CHANNEL, (T, 1): GATE_TOKEN}.get(tuple(gate.shape))
         if kind is None:
-            raise ValueError(f"gate: expected shape {(T, 1)}, {(H,)} or {(T, H)}, got {tuple(gate.shape)}")
+            raise ValueError(f"gate: expected shape {(T, 1)}, {row} or {full}, got {tuple(gate.shape)}")
     h = _empty((T, H), dt, y) if h is None else _need(h, dt, (T, H), "h")
     n = _empty((T, H), torch.bfloat16, y) if n is None else _need(n, torch.bfloat16, (T, H), "n")
     if quantize:

@@ -18,25 +18,32 @@ int check(const GemmArgs& a, int out_dtype) {
   return MOE_OK;
 }
 
-// Which kernel. Grouped: by the lists' average length (a tile of 256 rows wastes less than
-// it gains from there on).
-// Dense: up to 64 rows, weights on the lanes; above, whichever is estimated to end first.
-// A wide pair spends 0.43 us on a block of a tile and about 4 us on the rest; a CTA of the
-// other form 0.35 us on a block of 64 rows when it has an SM to itself, 0.4 a CTA when two
-// share one, and 3.5 on the rest. (Splitting K over pairs of a wide tile, too, measured
-// slower than either: 15 us for 128 x 7168 x 3584 against 14.9 unsplit, 29 for 333 x 2016 x
-// 7184 against 18.8, the sum of 128 KB of partials a CTA and clusters of four or eight
-// whole SMs costing more than the blocks saved.)
-bool wide(const GemmArgs& a, int sm_count) {
-  if (a.offsets) return (long long)a.M >= 96LL * a.E;
-  if (a.M <= 64) return false;
-  const long long wide_tiles = (((long long)a.M - 1) / 256 + 1) * ((a.nbn + 1) / 2), pairs = sm_count / 2;
-  const long long wide_ns = 4000 + ((wide_tiles - 1) / pairs + 1) * a.nbk * 430;
-  const long long tiles = (((long long)a.M - 1) / 64 + 1) * a.nbn;
-  const int n = fp8_impl::narrow_splits(tiles, a.nbk, sm_count);
-  const long long waves = (tiles * n - 1) / sm_count + 1;
-  const long long narrow_ns = 3500 + waves * ((a.nbk - 1) / n + 1) * (n > 1 ? 400 : 350);
-  return wide_ns < narrow_ns;
+// The kernel: 0 for the wide one, else the narrow one's rows a tile.
+// Grouped, by the lists' average length: wide from 96 on (64 experts, N = 4096, K = 3584: 64
+// rows 177 us narrow and 193 wide, 96 rows 220 and 198); below, a tile for the rows of all but
+// the fullest experts, half as many again as the average and four (256 experts of 9 rows: 88
+// us with 32, 94 with 16; 64 experts of 8: 145 with 16, 146 with 32).
+// Dense, up to 64 rows: the narrowest tile that holds them. Above, whatever is estimated to
+// end first: 0.43 us for a block of a wide tile and 4 us for the rest; 0.35 for a block of a
+// 64-row tile alone on an SM, 0.4 a CTA for two, and 3.5; 0.43 for one of a 128-row tile,
+// and 4 (5.5 where CTAs share a tile). (Splitting K over pairs of a wide tile, too,
+// measured slower: 15 us for 128 x 7168 x 3584 against 14.9 unsplit, 29 for 333 x 2016 x
+// 7184 against 18 by 64 rows, the sum of 128 KB of partials a CTA and clusters of four or
+// eight whole SMs costing more than the blocks saved.)
+int choose(const GemmArgs& a, int sm_count) {
+  if (a.offsets || a.M <= 64) {
+    if (a.offsets && (long long)a.M >= 96LL * a.E) return 0;
+    const long long want = a.offsets ? (3LL * a.M / 2 + a.E - 1) / a.E + 4 : a.M;
+    return want <= 16 ? 16 : want <= 32 ? 32 : 64;
+  }
+  const long long M = a.M, tiles0 = ((M - 1) / 256 + 1) * ((a.nbn + 1) / 2), pairs = sm_count / 2;
+  const long long ns0 = 4000 + ((tiles0 - 1) / pairs + 1) * a.nbk * 430;
+  const long long tiles64 = ((M - 1) / 64 + 1) * a.nbn, tiles128 = ((M - 1) / 128 + 1) * a.nbn;
+  const int s64 = fp8_impl::narrow_splits(64, tiles64, a.nbk, sm_count), s128 = fp8_impl::narrow_splits(128, tiles128, a.nbk, sm_count);
+  const long long ns64 = 3500 + ((tiles64 * s64 - 1) / sm_count + 1) * ((a.nbk - 1) / s64 + 1) * (s64 > 1 ? 400 : 350);
+  const long long ns128 = (s128 > 1 ? 5500 : 4000) + ((tiles128 * s128 - 1) / sm_count + 1) * ((a.nbk - 1) / s128 + 1) * 430;
+  if (ns0 <= ns64 && ns0 <= ns128) return 0;
+  return ns64 <= ns128 ? 64 : 128;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -91,7 +98,8 @@ int launch(GemmArgs& a, void* workspace, cudaStream_t stream) {
     if (st != MOE_OK) return st;
     a.a = copy, a.sa = scales, rows = a.M;
   }
-  return wide(a, dev.sm_count) ? fp8_impl::launch_wide(a, rows, dev.sm_count, stream) : fp8_impl::launch_narrow(a, rows, dev.sm_count, stream);
+  const int bn = choose(a, dev.sm_count);
+  return bn == 0 ? fp8_impl::launch_wide(a, rows, dev.sm_count, stream) : fp8_impl::launch_narrow(a, rows, bn, dev.sm_count, stream);
 }
 
 }  // namespace

@@ -8,8 +8,8 @@
 // TMEM slot (the accumulator starts anew), and the epilogue warps fold it into FP32
 // registers with the block's scales while the next stages multiply:
 //   - NG groups of 4 CG epilogue warps, one weight row (TMEM lane) and BN / CG columns per
-//     thread; with two groups they take the tiles in turn, each with TMEM slots of its
-//     own, so one tile's output and the next tile's first blocks overlap;
+//     thread; with two groups they take a persistent CTA's tiles in turn, each with TMEM
+//     slots of its own, so one tile's output and the next tile's first blocks overlap;
 //   - a TMA producer warp (a box of weights and one of rows a stage) and an MMA issuer warp;
 //   - a scale warp: the columns' scales of a block, times the weights' scale, to shared
 //     memory beside the block's TMEM slot (one barrier tells the epilogue of both).
@@ -35,8 +35,9 @@ struct Narrow {
   static constexpr int kEpiWarps = 4 * NG * CG;
   static constexpr int kThreads = 32 * (kEpiWarps + 3);
   static constexpr int kStageBytes = kWBytes + BN * FP8_BLOCK;
-  static constexpr int kSlots = BN <= 32 || NG == 1 ? 4 : 2;  // TMEM accumulators of a group
-  static constexpr int kTmemCols = NG * kSlots * BN;  // 64 .. 256
+  static constexpr int kSlots = NG * BN <= 64 ? 4 : 2;  // TMEM accumulators of a group
+  static constexpr int kTmemCols = NG * kSlots * BN;    // 64 .. 256
+  static constexpr int kPerSm = NG == 1 && BN <= 64 ? 2 : 1;  // CTAs an SM holds
   static constexpr int kScaleBytes = NG * kSlots * BN * 4;
 };
 
@@ -74,7 +75,7 @@ __device__ __forceinline__ void store(const GemmArgs& g, long long row, int n, f
 }
 
 template <int BN, bool GROUPED, int NG, int CG>
-__global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, NG == 1 ? 2 : 1)
+__global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, CG>::kPerSm)
     narrow_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const GemmArgs g,
                   long long a_rows, int stages, int S, int max_row_tiles) {
   using C = Narrow<BN, NG, CG>;
@@ -342,7 +343,7 @@ int launch(const GemmArgs& g, long long a_rows, int S, int stages, size_t smem, 
   if (!once.allow(reinterpret_cast<const void*>(kern), kMaxSmem - kStaticSmem)) return MOE_ERR_CUDA;
   const long long tiles = rows * g.nbn;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : (tiles < sm_count ? tiles : sm_count)));
+  cfg.gridDim = dim3((unsigned)(NG == 1 ? tiles * S : (tiles < sm_count ? tiles : sm_count)));
   cfg.blockDim = dim3(Narrow<BN, NG, CG>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -356,11 +357,63 @@ int launch(const GemmArgs& g, long long a_rows, int S, int stages, size_t smem, 
   return cudaLaunchKernelEx(&cfg, kern, tm_w, tm_a, g, a_rows, stages, S, (int)rows) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// The dense form whose CTAs share a tile: BN / 32 epilogue groups of 32 columns (more
+// accumulators a thread would leave no room for a second CTA), and the stages and shared
+// memory it takes at most.
+template <int BN>
+struct Split {
+  static constexpr int kParts = BN <= 32 ? 1 : BN / 32;
+  using C = Narrow<BN, 1, kParts>;
+  static constexpr int kShare = C::kPerSm > 1 ? kSmSmem / C::kPerSm : kMaxSmem;
+  static constexpr int kMost = (kShare - kStaticSmem - 1024 - C::kScaleBytes) / C::kStageBytes < kMaxStages
+                                   ? (kShare - kStaticSmem - 1024 - C::kScaleBytes) / C::kStageBytes
+                                   : kMaxStages;
+  static_assert((size_t)kMost * C::kStageBytes >= (size_t)BN * 512, "the stages hold a partial tile");
+};
+
+// Clusters of s such CTAs that are resident at once (clusters stay within a GPC, so whole-SM
+// CTAs leave some of its SMs over); looked up once.
+template <int BN>
+int max_clusters(int s) {
+  static std::atomic<int> known[kMaxSplits + 1];
+  int n = known[s].load(std::memory_order_relaxed);
+  if (n != 0) return n;
+  using P = Split<BN>;
+  auto kern = narrow_kernel<BN, false, 1, P::kParts>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(s * 64);
+  cfg.blockDim = dim3(P::C::kThreads);
+  cfg.dynamicSmemBytes = P::kShare - kStaticSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = s, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - kStaticSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (n <= 0) n = -1;
+  known[s].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// The CTAs of a tile: the most whose clusters are all resident at once where a CTA takes an
+// SM; where two share one, as many as there are places (a few clusters then wait for a
+// place: 1 x 7168 x 3584 took 6.0 us so and 6.5 with one CTA less a tile, 32 rows 7.4 and 9.3).
+template <int BN>
+int splits(long long tiles, int nbk, int sm_count) {
+  using C = typename Split<BN>::C;
+  for (int s = kMaxSplits; s >= 2; --s)
+    if (s <= nbk && (C::kPerSm > 1 ? tiles * s <= (long long)C::kPerSm * sm_count : tiles <= max_clusters<BN>(s))) return s;
+  return 1;
+}
+
 template <int BN, bool GROUPED>
 int plan(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t stream) {
   constexpr int kGroups = 2;
-  constexpr int kHalves = BN == 64 ? 2 : 1;  // (64 accumulators a thread would leave room for one CTA an SM)
-  using One = Narrow<BN, 1, kHalves>;
+  using One = typename Split<BN>::C;
   using Many = Narrow<BN, kGroups, 1>;
   // row tiles (grouped: at most, of ascending offsets)
   const long long rows = GROUPED ? (long long)g.M / BN + (g.E < g.M ? g.E : g.M) : ((long long)g.M + BN - 1) / BN;
@@ -375,23 +428,24 @@ int plan(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t stream)
   };
   if constexpr (!GROUPED) {
     // Split K while there are SMs without work: into the most parts whose CTAs are resident
-    // at once, two per SM (a part's blocks need not all have a stage).
-    constexpr int kMost = (kSmSmem / 2 - kStaticSmem - 1024 - One::kScaleBytes) / One::kStageBytes;
-    static_assert((size_t)kMost * One::kStageBytes >= (size_t)BN * 512, "the stages hold a partial tile");
-    const int s = narrow_splits(tiles, g.nbk, sm_count);
-    if (s > 1) {
+    // at once (a part's blocks need not all have a stage).
+    const int s = splits<BN>(tiles, g.nbk, sm_count);
+    if (s > 1 || BN > 64) {
       const int kbs = (g.nbk + s - 1) / s;
-      int st = kbs < kMost ? kbs : kMost;
+      int st = kbs < Split<BN>::kMost ? kbs : Split<BN>::kMost;
       while ((size_t)st * One::kStageBytes < (size_t)BN * 512) ++st;
-      return launch<BN, false, 1, kHalves>(g, a_rows, s, st, shared(One::kScaleBytes, st, One::kStageBytes, One::kTmemCols), rows,
-                                  sm_count, stream);
+      return launch<BN, false, 1, Split<BN>::kParts>(g, a_rows, s, st, shared(One::kScaleBytes, st, One::kStageBytes, One::kTmemCols),
+                                          rows, sm_count, stream);
     }
   }
-  const size_t extra = Many::kScaleBytes + (GROUPED ? 2 * (g.E + 1) * 4 : 0);
-  int stages = (int)((kMaxSmem - kStaticSmem - 1024 - extra) / Many::kStageBytes);
-  if (stages > kMaxStages) stages = kMaxStages;
-  return launch<BN, GROUPED, kGroups, 1>(g, a_rows, 1, stages, shared(extra, stages, Many::kStageBytes, Many::kTmemCols), rows,
-                                      sm_count, stream);
+  if constexpr (BN <= 64) {
+    const size_t extra = Many::kScaleBytes + (GROUPED ? 2 * (g.E + 1) * 4 : 0);
+    int stages = (int)((kMaxSmem - kStaticSmem - 1024 - extra) / Many::kStageBytes);
+    if (stages > kMaxStages) stages = kMaxStages;
+    return launch<BN, GROUPED, kGroups, 1>(g, a_rows, 1, stages, shared(extra, stages, Many::kStageBytes, Many::kTmemCols),
+                                           rows, sm_count, stream);
+  }
+  return MOE_ERR_INVALID_ARGUMENT;  // (not reached)
 }
 
 template <bool GROUPED>
@@ -399,25 +453,20 @@ int launch_bn(int bn, const GemmArgs& g, long long a_rows, int sm_count, cudaStr
   switch (bn) {
     case 16: return plan<16, GROUPED>(g, a_rows, sm_count, stream);
     case 32: return plan<32, GROUPED>(g, a_rows, sm_count, stream);
-    default: return plan<64, GROUPED>(g, a_rows, sm_count, stream);
+    case 64: return plan<64, GROUPED>(g, a_rows, sm_count, stream);
+    default:
+      if constexpr (!GROUPED) return plan<128, false>(g, a_rows, sm_count, stream);
+      return MOE_ERR_INVALID_ARGUMENT;
   }
 }
 
 }  // namespace
 
-int narrow_splits(long long tiles, int nbk, int sm_count) {
-  for (int s = kMaxSplits; s >= 2; --s)
-    if (s <= nbk && tiles * s <= 2LL * sm_count) return s;
-  return 1;
+int narrow_splits(int bn, long long tiles, int nbk, int sm_count) {
+  return bn > 64 ? splits<128>(tiles, nbk, sm_count) : splits<64>(tiles, nbk, sm_count);
 }
 
-int launch_narrow(const GemmArgs& g, long long rows, int sm_count, cudaStream_t stream) {
-  // dense: the narrowest tile that holds every row; grouped: the rows of all but the fullest
-  // experts, half as many again as the average and four (256 experts of 9 rows: 88 us with 32
-  // columns, 94 with 16; 64 experts of 8: 145 with 16, 146 with 32)
-  const long long want = g.offsets ? (3LL * g.M / 2 + g.E - 1) / g.E + 4 : g.M;
-  int bn = 16;
-  while (bn < 64 && bn < want) bn *= 2;
+int launch_narrow(const GemmArgs& g, long long rows, int bn, int sm_count, cudaStream_t stream) {
   return g.offsets ? launch_bn<true>(bn, g, rows, sm_count, stream) : launch_bn<false>(bn, g, rows, sm_count, stream);
 }
 

@@ -39,6 +39,8 @@ constexpr int kStageBytes = 2 * kHalf;
 constexpr int kStages = 5;
 constexpr int kSlots = 2;                     // TMEM accumulators of each half of the columns: all 512 columns
 constexpr int kScaleBytes = kSlots * 2 * 128 * 4;
+constexpr int kPadCols = 16;                  // columns of a warp's pad, 32 rows of it
+constexpr int kPadBytes = kEpiWarps * 32 * (kPadCols + 1) * 4;
 
 struct Tile {
   int e, n0, pos, cnt;  // expert, first weight row, this CTA's first row and its rows (may be <= 0)
@@ -104,8 +106,10 @@ __device__ __forceinline__ void transpose4(uint32_t (&u)[4][8]) {
 // The warp's 64 columns from n on of its 32 rows (`row` this lane's, -1: none). With whole,
 // 32-byte aligned pieces (vec) four lanes exchange theirs first, so that a store covers 128
 // contiguous bytes of eight rows and not 32 of all 32 (those took an eighth of the time of
-// 4096 x 7168 x 3584); else one by one.
-__device__ __forceinline__ void store_rows(const GemmArgs& g, long long row, int n, const float (&acc)[64], bool vec) {
+// 4096 x 7168 x 3584); else by way of the warp's pad in shared memory, 16 columns of two rows
+// a store (one value of 32 rows a store took 45 us for 500 x 1000 x 3008).
+__device__ __forceinline__ void store_rows(const GemmArgs& g, long long row, int n, const float (&acc)[64], bool vec,
+                                           float (*pad)[kPadCols + 1]) {
   const int lane = threadIdx.x & 31;
   if (vec) {
     uint32_t u[4][8];
@@ -129,17 +133,25 @@ __device__ __forceinline__ void store_rows(const GemmArgs& g, long long row, int
       for (int i = 0; i < 32; ++i) u[i >> 3][i & 7] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
       store4(2, n);
     }
-  } else if (row >= 0) {
-    if (g.f32) {
-      float* o = static_cast<float*>(g.out) + row * g.N + n;
+  } else {
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (n + i < g.N) o[i] = acc[i];
-    } else {
-      uint16_t* o = static_cast<uint16_t*>(g.out) + row * g.N + n;
+    for (int c0 = 0; c0 < 64; c0 += kPadCols) {
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (n + i < g.N) o[i] = f32_to_bf16(acc[i]);
+      for (int i = 0; i < kPadCols; ++i) pad[lane][i] = acc[c0 + i];
+      __syncwarp();
+      const int c = n + c0 + lane % kPadCols;
+#pragma unroll 4
+      for (int i = 0; i < kPadCols; ++i) {
+        const int l = 2 * i + lane / kPadCols;  // the lane whose row this is
+        const long long r = __shfl_sync(kFullMask, row, l);
+        const float v = pad[l][lane % kPadCols];
+        if (r < 0 || c >= g.N) continue;
+        if (g.f32)
+          static_cast<float*>(g.out)[r * g.N + c] = v;
+        else
+          static_cast<uint16_t*>(g.out)[r * g.N + c] = f32_to_bf16(v);
+      }
     }
   }
 }
@@ -157,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const mem = smem_raw + (base - raw);
   float* const scale_mem = reinterpret_cast<float*>(mem + kStages * kStageBytes);  // [slot][weight block][row]
-  int* const table = reinterpret_cast<int*>(mem + kStages * kStageBytes + kScaleBytes);
+  auto* const pads = reinterpret_cast<float(*)[32][kPadCols + 1]>(mem + kStages * kStageBytes + kScaleBytes);  // [warp]
+  int* const table = reinterpret_cast<int*>(mem + kStages * kStageBytes + kScaleBytes + kPadBytes);
   auto full = [&](int i) { return smem_u32(&bars[i]); };  // (the leader's: both CTAs' bytes)
   auto empty = [&](int i) { return smem_u32(&bars[kStages + i]); };
   // (slot, column half): sums and scales are there; they are read, as the issuer (the
@@ -351,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (kb + 1 < g.nbk && ok) fold(1);
       }
       if (!ok) break;
-      if (n < g.N) store_rows(g, out, n, acc, vec && n + 64 <= g.N);
+      if (n < g.N) store_rows(g, out, n, acc, vec && n + 64 <= g.N, pads[warp]);
       __syncwarp();
     }
   }
@@ -371,7 +384,7 @@ int launch(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t strea
   const long long rows = GROUPED ? (long long)g.M / kRows + (g.E < g.M ? g.E : g.M) : ((long long)g.M - 1) / kRows + 1;
   const long long tiles = rows * ((g.nbn + 1) / 2);
   if (tiles >= (1LL << 31) - (1 << 16) || rows >= kMaxRowTiles) return MOE_ERR_CAPACITY;
-  static_assert(1024 + kStages * kStageBytes + kScaleBytes + (MOE_MAX_EXPERTS + 1) * 4 + kStaticSmem <= kMaxSmem, "");
+  static_assert(1024 + kStages * kStageBytes + kScaleBytes + kPadBytes + (MOE_MAX_EXPERTS + 1) * 4 + kStaticSmem <= kMaxSmem, "");
   // All the shared memory a CTA may have: the pair holds both SMs' TMEM whole, so nothing
   // that allocates TMEM may share them.
   const size_t smem = kMaxSmem - kStaticSmem;
