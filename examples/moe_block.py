@@ -72,7 +72,7 @@ class MoeBlock:
         self.lists_ws = u8(max(1, moe.build_routing_lists_workspace(T, K, E)))
         self.latent, self.lq, self.ls = b16(T, L), u8(T, L), f32(T, nb(L))
         self.gu, self.aq, self.as_ = b16(P, 2 * F), u8(P, F), f32(P, nb(F))
-        self.gu_ws = u8(max(1, moe.expert_gemm_workspace(P, L)))
+        self.gu_ws = u8(max(1, moe.expert_gemm_workspace(P, E, 2 * F, L)))
         self.rows, self.routed, self.rq, self.rs = b16(P, L), b16(T, L), u8(T, L), f32(T, nb(L))
         self.y = b16(T, H)
 

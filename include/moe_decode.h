@@ -517,10 +517,11 @@ int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, co
  *   w, w_scales  device, E4M3 [E, N, K], FP32 [E, nb(N), nb(K)]
  *   offsets      device, int32 [E + 1]; pairs device, int32 [n_pairs]
  *   out          device, [n_pairs, N] of out_dtype
- *   workspace    device scratch of at least moe_expert_gemm_workspace(n_pairs, K, in_rows)
- *                bytes, 16-byte aligned; clobbered. Rows that do not lie in list order are
- *                copied there first; with in_rows MOE_ROWS_LIST it is 0, and NULL is
- *                allowed. Calls that share a workspace must not overlap.
+ *   workspace    device scratch of at least moe_expert_gemm_workspace(n_pairs, E, N, K,
+ *                in_rows) bytes, 16-byte aligned; clobbered. Rows that do not lie in list
+ *                order are copied there first where the lists are long; else, and with
+ *                MOE_ROWS_LIST, it is 0, and NULL is allowed. Calls that share a workspace
+ *                must not overlap.
  * n_pairs is the length of the list (T * topk). Rows of out that no listed pair names
  * are left as they are. A pair code outside [0, n_pairs), or an input row outside
  * [0, a_rows), is skipped and sets MOE_DEVERR_ROW_INDEX; offsets outside [0, n_pairs]
@@ -531,7 +532,7 @@ int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, co
 #define MOE_ROWS_TOKEN 0
 #define MOE_ROWS_LIST 1
 #define MOE_ROWS_PAIR 2
-size_t moe_expert_gemm_workspace(int n_pairs, int K, int in_rows);
+size_t moe_expert_gemm_workspace(int n_pairs, int E, int N, int K, int in_rows);
 int moe_expert_gemm(const uint8_t* a, const float* a_scales, int64_t a_rows, const uint8_t* w, const float* w_scales,
                     const int32_t* offsets, const int32_t* pairs, int n_pairs, int topk, int in_rows, int out_rows,
                     void* out, int out_dtype, int E, int N, int K, void* workspace, size_t workspace_bytes,

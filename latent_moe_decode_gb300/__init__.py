@@ -72,7 +72,7 @@ SIGNATURES = {
     "fp8_block_quantize_rows": (_I, [_P, _L, _I, _I, _P, _P, _I, _P]),
     "fp8_block_quantize_swiglu": (_I, [_P, _L, _I, _I, _P, _P, _I, _P]),
     "fp8_block_gemm": (_I, [_P] * 5 + [_I] * 4 + [_P]),
-    "moe_expert_gemm_workspace": (_SZ, [_I, _I, _I]),
+    "moe_expert_gemm_workspace": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_expert_gemm": (_I, [_P, _P, _L, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P, _SZ, _P]),
     "moe_block_norm": (_I, [_P, _L, _P, _I, _P, _P, _I, _P, _F, _F, _I, _I, _P, _P, _P, _P, _P]),
 }
@@ -488,8 +488,8 @@ def fp8_block_gemm(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16,
     return out
 
 
-def expert_gemm_workspace(n_pairs: int, K: int, in_rows: int = ROWS_TOKEN) -> int:
-    return int(load().moe_expert_gemm_workspace(n_pairs, K, in_rows))
+def expert_gemm_workspace(n_pairs: int, E: int, N: int, K: int, in_rows: int = ROWS_TOKEN) -> int:
+    return int(load().moe_expert_gemm_workspace(n_pairs, E, N, K, in_rows))
 
 
 def expert_gemm(a, a_scales, w, w_scales, offsets, pairs, topk: int, in_rows: int = ROWS_TOKEN,
@@ -509,7 +509,7 @@ def expert_gemm(a, a_scales, w, w_scales, offsets, pairs, topk: int, in_rows: in
     _need(pairs, torch.int32, (P,), "pairs")
     dt, code = _out_dtype(out, out_dtype)
     out = _empty((P, N), dt, a) if out is None else _need(out, dt, (P, N), "out")
-    need = expert_gemm_workspace(P, K, in_rows)
+    need = expert_gemm_workspace(P, E, N, K, in_rows)
     if need and workspace is None:
         workspace = _empty((need,), torch.uint8, a)
     wb = 0 if workspace is None else workspace.numel() * workspace.element_size()

@@ -30,12 +30,14 @@ int check(const GemmArgs& a, int out_dtype) {
 // measured slower: 15 us for 128 x 7168 x 3584 against 14.9 unsplit, 29 for 333 x 2016 x
 // 7184 against 18 by 64 rows, the sum of 128 KB of partials a CTA and clusters of four or
 // eight whole SMs costing more than the blocks saved.)
+int choose_listed(int n_pairs, int E) {
+  if (n_pairs >= 96LL * E) return 0;
+  const long long want = (3LL * n_pairs / 2 + E - 1) / E + 4;
+  return want <= 16 ? 16 : want <= 32 ? 32 : 64;
+}
 int choose(const GemmArgs& a, int sm_count) {
-  if (a.offsets || a.M <= 64) {
-    if (a.offsets && (long long)a.M >= 96LL * a.E) return 0;
-    const long long want = a.offsets ? (3LL * a.M / 2 + a.E - 1) / a.E + 4 : a.M;
-    return want <= 16 ? 16 : want <= 32 ? 32 : 64;
-  }
+  if (a.offsets) return choose_listed(a.M, a.E);
+  if (a.M <= 64) return a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64;
   const long long M = a.M, tiles0 = ((M - 1) / 256 + 1) * ((a.nbn + 1) / 2), pairs = sm_count / 2;
   const long long ns0 = 4000 + ((tiles0 - 1) / pairs + 1) * a.nbk * 430;
   const long long tiles64 = ((M - 1) / 64 + 1) * a.nbn, tiles128 = ((M - 1) / 128 + 1) * a.nbn;
@@ -47,6 +49,16 @@ int choose(const GemmArgs& a, int sm_count) {
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Whether rows that do not lie in list order are copied there before the product: always for
+// the wide kernel, which reads boxes of them; for the narrow one, whose warp fetches single
+// rows at 16 a tile as fast as HBM brings the weights, and at 32 not quite (1020 tokens x 16
+// of 896 experts, N = 3584, K = 1024: 546 us, 505 with the copies), from where that costs
+// more than the copies' launch: some 50 us of weights.
+bool copies(int n_pairs, int E, int N, int K, int in_rows) {
+  const int bn = choose_listed(n_pairs, E);
+  return in_rows != MOE_ROWS_LIST && (bn == 0 || (bn > 16 && (double)E * N * K > 256e6));
+}
 
 // Copies of the listed pairs' rows and scales in list order.
 size_t list_copy_bytes(int n_pairs, int K) {
@@ -90,16 +102,17 @@ int launch(GemmArgs& a, void* workspace, cudaStream_t stream) {
   if (st != MOE_OK) return st;
   a.err = dev.error_word;
   long long rows = a.a_rows;
-  if (a.offsets && a.in_rows != MOE_ROWS_LIST) {
+  const int bn = choose(a, dev.sm_count);
+  bool named = a.offsets && a.in_rows != MOE_ROWS_LIST;
+  if (a.offsets && copies(a.M, a.E, a.N, a.K, a.in_rows)) {
     uint8_t* copy = static_cast<uint8_t*>(workspace);
     float* scales = reinterpret_cast<float*>(copy + align256((size_t)a.M * a.K));
     const long long need = ((long long)a.M * 32 + kCopyThreads - 1) / kCopyThreads, most = 8LL * dev.sm_count;
     st = launch_pdl(list_copy_kernel, dim3((unsigned)(need < most ? need : most)), dim3(kCopyThreads), 0, stream, a, copy, scales);
     if (st != MOE_OK) return st;
-    a.a = copy, a.sa = scales, rows = a.M;
+    a.a = copy, a.sa = scales, rows = a.M, named = false;
   }
-  const int bn = choose(a, dev.sm_count);
-  return bn == 0 ? fp8_impl::launch_wide(a, rows, dev.sm_count, stream) : fp8_impl::launch_narrow(a, rows, bn, dev.sm_count, stream);
+  return bn == 0 ? fp8_impl::launch_wide(a, rows, dev.sm_count, stream) : fp8_impl::launch_narrow(a, rows, named, bn, dev.sm_count, stream);
 }
 
 }  // namespace
@@ -116,8 +129,8 @@ extern "C" int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uin
   return launch(g, nullptr, as_cuda(stream));
 }
 
-extern "C" size_t moe_expert_gemm_workspace(int n_pairs, int K, int in_rows) {
-  if (n_pairs < 1 || K < 16 || in_rows == MOE_ROWS_LIST) return 0;
+extern "C" size_t moe_expert_gemm_workspace(int n_pairs, int E, int N, int K, int in_rows) {
+  if (n_pairs < 1 || E < 1 || N < 1 || K < 16 || !moe::copies(n_pairs, E, N, K, in_rows)) return 0;
   return moe::list_copy_bytes(n_pairs, K);
 }
 
@@ -138,7 +151,7 @@ extern "C" int moe_expert_gemm(const uint8_t* a, const float* a_scales, int64_t 
   if (!offsets || !pairs) return MOE_ERR_INVALID_ARGUMENT;
   if (E > MOE_MAX_EXPERTS) return MOE_ERR_CAPACITY;
   if (!aligned(offsets, 4) || !aligned(pairs, 4) || !aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
-  const size_t need = moe_expert_gemm_workspace(n_pairs, K, in_rows);
+  const size_t need = moe_expert_gemm_workspace(n_pairs, E, N, K, in_rows);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
   return launch(g, workspace, as_cuda(stream));
 }

@@ -32,8 +32,9 @@ struct GemmArgs {
 // The two kernels. g.a and g.sa hold `rows` rows, grouped in list order (in_rows and
 // a_rows say which rows of the caller's they are, and so which pairs are in range).
 // Few rows per weight tile: weights on the tensor core's 128 lanes, rows on its columns, bn
-// of them a tile (16, 32, 64; dense also 128).
-int launch_narrow(const GemmArgs& g, long long rows, int bn, int sm_count, cudaStream_t stream);
+// of them a tile (16, 32, 64; dense also 128). named: g.a and g.sa are the caller's, their
+// rows to be fetched as the pairs name them.
+int launch_narrow(const GemmArgs& g, long long rows, bool named, int bn, int sm_count, cudaStream_t stream);
 // CTAs that a dense narrow product of `tiles` tiles of bn (64 or 128) rows puts to work on each.
 int narrow_splits(int bn, long long tiles, int nbk, int sm_count);
 // Many: rows on the lanes, weights on the columns, two SMs per tile.

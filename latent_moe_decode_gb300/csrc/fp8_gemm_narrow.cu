@@ -11,15 +11,15 @@
 //     thread; with two groups they take a persistent CTA's tiles in turn, each with TMEM
 //     slots of its own, so one tile's output and the next tile's first blocks overlap;
 //   - a TMA producer warp (a box of weights and one of rows a stage) and an MMA issuer warp;
+//     rows that an expert's list names one by one are copied by a warp of their own;
 //   - a scale warp: the columns' scales of a block, times the weights' scale, to shared
 //     memory beside the block's TMEM slot (one barrier tells the epilogue of both).
 // Dense: tiles with fewer than two per SM split K over a cluster of S CTAs, whose scaled
 // partials are summed in rank order through distributed shared memory. Grouped: a
 // persistent grid walks the tiles (expert, weight tile, row tile), found in a table of
-// tile counts that every CTA builds from the offsets. The rows lie in list order (copied
-// there first where they do not): TMA's gather4 took 72 cycles for four rows, so that at
-// 32 rows a tile the copies and not HBM set the pace (885 us for 1020 tokens x 16 of 896
-// experts).
+// tile counts that every CTA builds from the offsets. (TMA's gather4 for the named rows
+// took 72 cycles for four, so that at 32 rows a tile the copies and not HBM set the pace:
+// 885 us for 1020 tokens x 16 of 896 experts against 505.)
 #include "fp8_gemm.cuh"
 
 namespace moe {
@@ -30,10 +30,14 @@ constexpr int kWBytes = 128 * FP8_BLOCK;  // the weights of a stage
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplits = 8;
 
-template <int BN, int NG, int CG>
+// Where the rows of a tile come from: consecutive rows of a; consecutive positions of an
+// expert's list, rows in list order; or the rows that the list's pairs name.
+enum Rows { kDense, kListed, kNamed };
+
+template <int BN, Rows ROWS, int NG, int CG>
 struct Narrow {
   static constexpr int kEpiWarps = 4 * NG * CG;
-  static constexpr int kThreads = 32 * (kEpiWarps + 3);
+  static constexpr int kThreads = 32 * (kEpiWarps + (ROWS == kNamed ? 4 : 3));
   static constexpr int kStageBytes = kWBytes + BN * FP8_BLOCK;
   static constexpr int kSlots = NG * BN <= 64 ? 4 : 2;  // TMEM accumulators of a group
   static constexpr int kTmemCols = NG * kSlots * BN;    // 64 .. 256
@@ -46,10 +50,10 @@ struct Tile {
 };
 
 // Grouped: table[0 .. E] the experts' first tiles, table[E + 1 ..] their first positions.
-template <int BN, bool GROUPED>
+template <int BN, Rows ROWS>
 __device__ __forceinline__ Tile tile_at(const GemmArgs& g, const int* table, int t) {
   Tile r;
-  if constexpr (GROUPED) {
+  if constexpr (ROWS != kDense) {
     // row tiles of one weight tile are neighbours: they meet its weights in L2
     r.e = tile_expert(table, g.E, t / g.nbn);
     const int c = table[r.e + 1] - table[r.e], local = t - table[r.e] * g.nbn;
@@ -74,11 +78,12 @@ __device__ __forceinline__ void store(const GemmArgs& g, long long row, int n, f
     static_cast<uint16_t*>(g.out)[row * g.N + n] = f32_to_bf16(v);
 }
 
-template <int BN, bool GROUPED, int NG, int CG>
-__global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, CG>::kPerSm)
+template <int BN, Rows ROWS, int NG, int CG>
+__global__ void __launch_bounds__(Narrow<BN, ROWS, NG, CG>::kThreads, Narrow<BN, ROWS, NG, CG>::kPerSm)
     narrow_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const GemmArgs g,
                   long long a_rows, int stages, int S, int max_row_tiles) {
-  using C = Narrow<BN, NG, CG>;
+  using C = Narrow<BN, ROWS, NG, CG>;
+  constexpr bool GROUPED = ROWS != kDense;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 3 * NG * C::kSlots];
   __shared__ uint32_t tmem_slot;
@@ -97,7 +102,7 @@ __global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, C
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
-      mbar_init(full(i), 1);
+      mbar_init(full(i), ROWS == kNamed ? 33 : 1);  // the boxes' bytes; each lane's share of the named rows
       mbar_init(empty(i), 1);
     }
     for (int i = 0; i < NG * C::kSlots; ++i) {
@@ -139,16 +144,16 @@ __global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, C
     int issued = 0;
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
-      const Tile ti = tile_at<BN, GROUPED>(g, table, t);
+      const Tile ti = tile_at<BN, ROWS>(g, table, t);
       const int wrow = ti.e * g.N + ti.n0;
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = __all_sync(kFullMask, mbar_wait_asleep(empty(st.slot), st.lap ^ 1u, g.err));
         if (!ok) break;
         const uint32_t dst = base + st.slot * C::kStageBytes, bar = full(st.slot);
         if (elect_one()) {
-          mbar_expect_tx(bar, C::kStageBytes);
+          mbar_expect_tx(bar, ROWS == kNamed ? kWBytes : C::kStageBytes);
           tma_load_2d(dst, &tm_w, kb * FP8_BLOCK, wrow, bar);
-          tma_load_2d(dst + kWBytes, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
+          if (ROWS != kNamed) tma_load_2d(dst + kWBytes, &tm_a, kb * FP8_BLOCK, ti.pos, bar);
         }
         __syncwarp();
         st.next(stages);
@@ -172,6 +177,8 @@ __global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, C
         const int sl = grp * C::kSlots + (int)(i & kMask);
         ok = __all_sync(kFullMask, mbar_wait_asleep(tempty(sl), lap(i) ^ 1u, g.err) && mbar_wait_asleep(full(st.slot), st.lap, g.err));
         if (!ok) break;
+        // (the named rows were not written by the proxy that reads them)
+        if (ROWS == kNamed) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tcgen05_after_sync();
         const uint64_t at = (uint64_t)(st.slot * (C::kStageBytes >> 4));
         if (elect_one()) {
@@ -193,15 +200,33 @@ __global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, C
     uint32_t at0 = 0, at1 = 0;
     int grp = 0;
     bool ok = true;
+    int code[CL] = {};  // pair codes of the tile's columns: those of the next tile are looked up under the present one
+    auto look = [&](const Tile& ti) {
+#pragma unroll
+      for (int i = 0; i < CL; ++i) code[i] = lane + 32 * i < ti.cnt ? __ldg(g.pairs + ti.pos + lane + 32 * i) : 0;
+    };
+    Tile ti = {0, 0, 0, 0};
+    if (t0 < tiles) {
+      ti = tile_at<BN, ROWS>(g, table, t0);
+      if (ROWS == kNamed) look(ti);
+    }
     for (int t = t0; t < tiles && ok; t += step) {
-      const Tile ti = tile_at<BN, GROUPED>(g, table, t);
       const float* sap[CL];
 #pragma unroll
       for (int i = 0; i < CL; ++i) {
         const int c = lane + 32 * i;
-        sap[i] = c < ti.cnt && ti.pos + c < a_rows ? g.sa + (long long)(ti.pos + c) * g.nbk : nullptr;
+        long long in = ti.pos + c, out;
+        if (c >= ti.cnt)
+          in = -1;
+        else if (ROWS == kNamed)
+          code_rows(g, ti.pos + c, code[i], &in, &out);
+        sap[i] = in >= 0 && in < a_rows ? g.sa + in * g.nbk : nullptr;
       }
       const float* swp = g.sw + ((long long)ti.e * g.nbn + ti.n0 / FP8_BLOCK) * g.nbk;
+      if (t + step < tiles) {
+        ti = tile_at<BN, ROWS>(g, table, t + step);
+        if (ROWS == kNamed) look(ti);
+      }
       float s[CL], b = 0.f;
       auto fetch = [&](int kb) {
         b = __ldg(swp + kb);
@@ -224,6 +249,55 @@ __global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, C
       if (grp) at1 = i; else at0 = i;
       if (NG == 2) grp ^= 1;
     }
+  } else if (ROWS == kNamed && warp == C::kEpiWarps + 3) {  // named rows
+    // A lane copies 16 bytes of rows lane / 8 + 4 j: a row's 128 bytes by eight lanes, to the
+    // places that the 128-byte swizzle gives them. The copies themselves arrive on the
+    // stage's barrier, so as many stages are on their way as there are.
+    constexpr int R = BN / 4;
+    const int chunk = lane & 7, row0 = lane >> 3;
+    Ring st;
+    bool ok = true;
+    int code[R] = {};
+    auto look = [&](const Tile& ti) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) code[j] = row0 + 4 * j < ti.cnt ? __ldg(g.pairs + ti.pos + row0 + 4 * j) : 0;
+    };
+    Tile ti = {0, 0, 0, 0};
+    if (t0 < tiles) {
+      ti = tile_at<BN, ROWS>(g, table, t0);
+      look(ti);
+    }
+    for (int t = t0; t < tiles && ok; t += step) {
+      const uint8_t* src[R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const int c = row0 + 4 * j;
+        long long in = -1, out;
+        if (c < ti.cnt) code_rows(g, ti.pos + c, code[j], &in, &out);
+        src[j] = in < 0 ? nullptr : g.a + in * g.K + 16 * chunk;
+      }
+      if (t + step < tiles) {
+        ti = tile_at<BN, ROWS>(g, table, t + step);
+        look(ti);
+      }
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = __all_sync(kFullMask, mbar_wait_asleep(empty(st.slot), st.lap ^ 1u, g.err));
+        if (!ok) break;
+        const uint32_t dst = base + st.slot * C::kStageBytes + kWBytes + row0 * FP8_BLOCK;
+        const bool in_k = kb * FP8_BLOCK + 16 * chunk < g.K;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          const int row = row0 + 4 * j;
+          const bool in = src[j] != nullptr && in_k;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 4 * FP8_BLOCK * j + 16 * (chunk ^ (row & 7))),
+                       "l"(in ? src[j] + (size_t)kb * FP8_BLOCK : g.a), "r"(in ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full(st.slot)) : "memory");
+        st.next(stages);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (a CTA that gave up leaves none behind)
   } else {  // epilogue
     constexpr int CW = BN / CG;           // columns of a thread
     constexpr int CL = (CW + 31) / 32;
@@ -234,7 +308,7 @@ __global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, C
     uint32_t i = 0;
     bool ok = true;
     for (int t = t0 + grp * step; t < tiles && ok; t += NG * step) {
-      const Tile ti = tile_at<BN, GROUPED>(g, table, t);
+      const Tile ti = tile_at<BN, ROWS>(g, table, t);
       int code[CL];  // (used only at the tile's end)
 #pragma unroll
       for (int j = 0; j < CL; ++j)
@@ -307,7 +381,7 @@ __global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, C
     __syncwarp();
     cluster_sync();  // every split's partial is written and visible
     if (warp < C::kEpiWarps) {
-      const Tile ti = tile_at<BN, GROUPED>(g, table, t0);
+      const Tile ti = tile_at<BN, ROWS>(g, table, t0);
       const int row = threadIdx.x & 127, n = ti.n0 + row;
       uint32_t peer[kMaxSplits];
 #pragma unroll
@@ -333,18 +407,18 @@ __global__ void __launch_bounds__(Narrow<BN, NG, CG>::kThreads, Narrow<BN, NG, C
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
 }
 
-template <int BN, bool GROUPED, int NG, int CG>
+template <int BN, Rows ROWS, int NG, int CG>
 int launch(const GemmArgs& g, long long a_rows, int S, int stages, size_t smem, long long rows, int sm_count, cudaStream_t stream) {
   CUtensorMap tm_w, tm_a;
   if (!make_code_map(&tm_w, g.w, (long long)g.E * g.N, g.K, 128)) return MOE_ERR_CUDA;
   if (!make_code_map(&tm_a, g.a, a_rows, g.K, BN)) return MOE_ERR_CUDA;
-  auto kern = narrow_kernel<BN, GROUPED, NG, CG>;
+  auto kern = narrow_kernel<BN, ROWS, NG, CG>;
   static OncePerDevice once;
   if (!once.allow(reinterpret_cast<const void*>(kern), kMaxSmem - kStaticSmem)) return MOE_ERR_CUDA;
   const long long tiles = rows * g.nbn;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(NG == 1 ? tiles * S : (tiles < sm_count ? tiles : sm_count)));
-  cfg.blockDim = dim3(Narrow<BN, NG, CG>::kThreads);
+  cfg.blockDim = dim3(Narrow<BN, ROWS, NG, CG>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -363,7 +437,7 @@ int launch(const GemmArgs& g, long long a_rows, int S, int stages, size_t smem, 
 template <int BN>
 struct Split {
   static constexpr int kParts = BN <= 32 ? 1 : BN / 32;
-  using C = Narrow<BN, 1, kParts>;
+  using C = Narrow<BN, kDense, 1, kParts>;
   static constexpr int kShare = C::kPerSm > 1 ? kSmSmem / C::kPerSm : kMaxSmem;
   static constexpr int kMost = (kShare - kStaticSmem - 1024 - C::kScaleBytes) / C::kStageBytes < kMaxStages
                                    ? (kShare - kStaticSmem - 1024 - C::kScaleBytes) / C::kStageBytes
@@ -379,7 +453,7 @@ int max_clusters(int s) {
   int n = known[s].load(std::memory_order_relaxed);
   if (n != 0) return n;
   using P = Split<BN>;
-  auto kern = narrow_kernel<BN, false, 1, P::kParts>;
+  auto kern = narrow_kernel<BN, kDense, 1, P::kParts>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(s * 64);
   cfg.blockDim = dim3(P::C::kThreads);
@@ -410,11 +484,12 @@ int splits(long long tiles, int nbk, int sm_count) {
   return 1;
 }
 
-template <int BN, bool GROUPED>
+template <int BN, Rows ROWS>
 int plan(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t stream) {
   constexpr int kGroups = 2;
+  constexpr bool GROUPED = ROWS != kDense;
   using One = typename Split<BN>::C;
-  using Many = Narrow<BN, kGroups, 1>;
+  using Many = Narrow<BN, ROWS, kGroups, 1>;
   // row tiles (grouped: at most, of ascending offsets)
   const long long rows = GROUPED ? (long long)g.M / BN + (g.E < g.M ? g.E : g.M) : ((long long)g.M + BN - 1) / BN;
   const long long tiles = rows * g.nbn;
@@ -434,7 +509,7 @@ int plan(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t stream)
       const int kbs = (g.nbk + s - 1) / s;
       int st = kbs < Split<BN>::kMost ? kbs : Split<BN>::kMost;
       while ((size_t)st * One::kStageBytes < (size_t)BN * 512) ++st;
-      return launch<BN, false, 1, Split<BN>::kParts>(g, a_rows, s, st, shared(One::kScaleBytes, st, One::kStageBytes, One::kTmemCols),
+      return launch<BN, kDense, 1, Split<BN>::kParts>(g, a_rows, s, st, shared(One::kScaleBytes, st, One::kStageBytes, One::kTmemCols),
                                           rows, sm_count, stream);
     }
   }
@@ -442,20 +517,20 @@ int plan(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t stream)
     const size_t extra = Many::kScaleBytes + (GROUPED ? 2 * (g.E + 1) * 4 : 0);
     int stages = (int)((kMaxSmem - kStaticSmem - 1024 - extra) / Many::kStageBytes);
     if (stages > kMaxStages) stages = kMaxStages;
-    return launch<BN, GROUPED, kGroups, 1>(g, a_rows, 1, stages, shared(extra, stages, Many::kStageBytes, Many::kTmemCols),
+    return launch<BN, ROWS, kGroups, 1>(g, a_rows, 1, stages, shared(extra, stages, Many::kStageBytes, Many::kTmemCols),
                                            rows, sm_count, stream);
   }
   return MOE_ERR_INVALID_ARGUMENT;  // (not reached)
 }
 
-template <bool GROUPED>
+template <Rows ROWS>
 int launch_bn(int bn, const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t stream) {
   switch (bn) {
-    case 16: return plan<16, GROUPED>(g, a_rows, sm_count, stream);
-    case 32: return plan<32, GROUPED>(g, a_rows, sm_count, stream);
-    case 64: return plan<64, GROUPED>(g, a_rows, sm_count, stream);
+    case 16: return plan<16, ROWS>(g, a_rows, sm_count, stream);
+    case 32: return plan<32, ROWS>(g, a_rows, sm_count, stream);
+    case 64: return plan<64, ROWS>(g, a_rows, sm_count, stream);
     default:
-      if constexpr (!GROUPED) return plan<128, false>(g, a_rows, sm_count, stream);
+      if constexpr (ROWS == kDense) return plan<128, kDense>(g, a_rows, sm_count, stream);
       return MOE_ERR_INVALID_ARGUMENT;
   }
 }
@@ -466,8 +541,9 @@ int narrow_splits(int bn, long long tiles, int nbk, int sm_count) {
   return bn > 64 ? splits<128>(tiles, nbk, sm_count) : splits<64>(tiles, nbk, sm_count);
 }
 
-int launch_narrow(const GemmArgs& g, long long rows, int bn, int sm_count, cudaStream_t stream) {
-  return g.offsets ? launch_bn<true>(bn, g, rows, sm_count, stream) : launch_bn<false>(bn, g, rows, sm_count, stream);
+int launch_narrow(const GemmArgs& g, long long rows, bool named, int bn, int sm_count, cudaStream_t stream) {
+  if (!g.offsets) return launch_bn<kDense>(bn, g, rows, sm_count, stream);
+  return named ? launch_bn<kNamed>(bn, g, rows, sm_count, stream) : launch_bn<kListed>(bn, g, rows, sm_count, stream);
 }
 
 }  // namespace fp8_impl

@@ -58,11 +58,12 @@ def test_expert_gemm(lib):
         assert f(**kw) == 1, kw
     assert f(E=4097) == 3
     assert f(a=P(264)) == 2 and f(off=OFF) == 2 and f(pairs=OFF) == 2 and f(ws=P(264)) == 2
-    # rows that are not in list order are copied there first
+    # rows of long lists that are not in list order are copied there first
     need = lib.moe_expert_gemm_workspace
-    assert need(100, 32, 1) == 0 and need(0, 32, 0) == 0 and need(100, 8, 0) == 0
-    assert need(100, 160, 0) >= 100 * 168 and need(100, 160, 2) == need(100, 160, 0)
-    assert f(n=100, wb=need(100, 32, 0) - 1) == 4 and f(n=100, ws=None) == 4
+    assert need(8, 4, 8, 32, 0) == 0 and need(1000, 4, 8, 32, 1) == 0 and need(0, 4, 8, 32, 0) == 0 and need(1000, 4, 8, 8, 0) == 0
+    assert need(1000, 4, 8, 160, 0) >= 1000 * 168 and need(1000, 4, 8, 160, 2) == need(1000, 4, 8, 160, 0)
+    assert need(1000, 64, 128, 1024, 0) == 0 and need(1000, 64, 4096, 1024, 0) >= 1000 * 1056  # (few weights; many)
+    assert f(n=1000, wb=need(1000, 4, 8, 32, 0) - 1) == 4 and f(n=1000, ws=None) == 4
 
 
 def test_block_norm(lib):

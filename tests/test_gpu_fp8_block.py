@@ -343,6 +343,27 @@ def test_expert_gemm_bad_offsets(moe):
     assert spans[3][0] > spans[3][1]
 
 
+@pytest.mark.parametrize("in_rows", ["ROWS_TOKEN", "ROWS_PAIR"])
+def test_expert_rows_copied_for_many_weights(moe, in_rows):
+    """Lists of some ten rows over more than 256 MB of weights: rows are copied to list order first."""
+    T, topk, E, N, K = 330, 2, 65, 1040, 4096
+    rng = np.random.default_rng(5)
+    ids = np.stack([rng.permutation(E)[:topk] for _ in range(T)])
+    rows = T if in_rows == "ROWS_TOKEN" else T * topk
+    a, sa, _, _ = operands(4, rows, 8, K)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = torch.randint(0, 0x78, (E, N, K), dtype=torch.uint8, device="cuda", generator=g)
+    sw = torch.full((E, ref.nb(N), ref.nb(K)), 0.001, device="cuda")
+    offsets, pairs = lists(ids, E)
+    assert moe.expert_gemm_workspace(T * topk, E, N, K, getattr(moe, in_rows)) > 0
+    out = moe.expert_gemm(dev(a), dev(sa), w, sw, dev(offsets), dev(pairs), topk, in_rows=getattr(moe, in_rows), out_dtype=torch.float32)
+    for e in (0, 31, 64):
+        p = pairs[offsets[e]:offsets[e + 1]]
+        src = p // topk if in_rows == "ROWS_TOKEN" else p
+        gemm_check(out[torch.from_numpy(p.astype(np.int64)).cuda()], a[src], sa[src], host(w[e]), host(sw[e]))
+    assert moe.device_error() == 0
+
+
 def test_expert_weights_past_32_bits(moe):
     """Weights of more than 2^32 bytes: the last experts are reached."""
     E, N, K, T = 1100, 2048, 2048, 3
