@@ -183,16 +183,15 @@ __global__ void __launch_bounds__(kMaxThreads<V>) block_norm_kernel(const BlockN
       float w[8];
       bf16x8_to_f32(next[i], w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(__fmul_rn(r[i][j], root), w[j]);
+      for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(r[i][j], w[j]);  // n = w * root
       if (a.n && f < nv)
-        st16(a.n + at + 8 * f, make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]),
-                                          pack_bf16x2(w[6], w[7])));
+        st16(a.n + at + 8 * f,
+             make_uint4(pack_bf16x2(__fmul_rn(w[0], root), __fmul_rn(w[1], root)), pack_bf16x2(__fmul_rn(w[2], root), __fmul_rn(w[3], root)),
+                        pack_bf16x2(__fmul_rn(w[4], root), __fmul_rn(w[5], root)), pack_bf16x2(__fmul_rn(w[6], root), __fmul_rn(w[7], root))));
       if (a.q) {
-        if (f >= nv) {  // (0 * infinity past the row's end)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = 0.f;
-        }
-        const BlockScale s = block_scale_shared(block_max(magnitude(w)));
+        // n / amax(n) = w / amax(w): the codes need neither the root nor its rounding
+        const float top = __uint_as_float(block_max(magnitude(w)));
+        const BlockScale s = block_scale_of_product(top, root);
         if (f < nv) {
           *reinterpret_cast<uint2*>(a.q + at + 8 * f) = encode8(w, s);
           if ((f & 15) == 0) a.scales[row * a.nb + (f >> 4)] = s.scale;

@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __re
   const int lane = threadIdx.x & 31, warps = gridDim.x * (kThreads / 32);
   grid_launch_dependents();
   grid_wait();
+  const uint64_t once = policy_evict_first();
   for (int u = (int)((blockIdx.x * kThreads + threadIdx.x) >> 5); u < units; u += warps) {
     const int row = u / runs, b0 = (u - row * runs) * kRun + (lane >> 4);  // this half-warp's first block
     const int col0 = b0 * FP8_BLOCK + 8 * (lane & 15);
@@ -48,8 +49,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __re
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const bool in = col0 + 2 * i * FP8_BLOCK < cols;
-      a[i] = in ? ld_nc16(p + 2 * i * FP8_BLOCK) : make_uint4(0, 0, 0, 0);
-      if (SWIGLU) b[i] = in ? ld_nc16(p + cols + 2 * i * FP8_BLOCK) : make_uint4(0, 0, 0, 0);
+      a[i] = in ? ld_stream16(p + 2 * i * FP8_BLOCK, once) : make_uint4(0, 0, 0, 0);
+      if (SWIGLU) b[i] = in ? ld_stream16(p + cols + 2 * i * FP8_BLOCK, once) : make_uint4(0, 0, 0, 0);
     }
     float v[kUnroll][8];
     uint32_t m[kUnroll];
