@@ -2,8 +2,8 @@
 // the groups of largest value, the top-K experts in them, renormalised weights.
 //
 // A token is 4 E bytes of logits and a few hundred dependent operations, so a call is
-// bound by latency (one token) and by issue (thousands): one warp per token, the row in
-// registers, no step that takes the warp once per choice.
+// bound by latency (one token) and by issue (thousands): one warp per token, no step that
+// takes the warp once per choice.
 //   - Keys are FP32 values mapped to integers of the same order (0: not to be chosen), so
 //     that NaN, infinities and dropped experts need no branches.
 //   - Groups: the warp's lanes divide into 32 / n_group lanes per group, scan the keys in
@@ -13,6 +13,9 @@
 //     key from below (K lanes hold a key at least that large). The experts at or above it, about
 //     K to 2 K, are compacted and ranked against each other by shuffles; more than 64 of
 //     them (heavy ties) take K rounds of a warp argmax instead.
+//   - Sigmoid scores without groups: keys from the hardware's approximate tanh, whose error
+//     (measured over all inputs, see topk.cuh) widens the bound; exact keys for the
+//     candidates alone.
 //   - Softmax without a bias and with groups by their maximum chooses by the logits, the
 //     order of the exact scores; its weights need the row's sum only when they are not
 //     renormalised (e / S over the sum of e / S).
@@ -86,68 +89,114 @@ constexpr int kList = 64;    // candidates it ranks
 
 struct RouteScratch {
   unsigned long long list[kList];  // candidates: (key, ~expert)
-  float x[kList];                  // ... and their logits
   int id[MOE_MAX_TOPK];            // the choice
   float s[MOE_MAX_TOPK];
 };
 
-// NJ experts a lane; VEC: expert 128 j + 4 lane + i in element 4 j + i (16-byte loads, no
-// group ends inside one), else expert 32 j + lane in element j. keys: E words of shared
-// memory (GROUPS).
+// NJ experts a lane; VEC: expert 128 j + 4 lane + i in element 4 j + i (16-byte accesses, no
+// group ends inside one), else expert 32 j + lane in element j. xs, keys: the token's logits
+// and keys (the bias, until they are made) in shared memory. Scores are made four a lane at a
+// time in a loop that is not unrolled: unrolled, its thousands of instructions, run once
+// a call, took longer to fetch than to execute (11 tokens x 672 experts 9.0 us).
 template <int NJ, bool VEC, bool GROUPS>
-__device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteScratch& ws, uint32_t* keys) {
+__device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteScratch& ws, float* xs, uint32_t* keys) {
   const int lane = threadIdx.x & 31, E = a.E, K = a.K;
   auto expert = [&](int j) { return VEC ? 128 * (j >> 2) + 4 * lane + (j & 3) : 32 * j + lane; };
   const float* row = a.logits + (size_t)t * E;
-  float x[NJ];
-  uint32_t key[NJ];
-  if constexpr (VEC) {
-#pragma unroll
-    for (int j = 0; j < NJ; j += 4) {
-      const float4 v = expert(j) < E ? __ldg(reinterpret_cast<const float4*>(row + expert(j))) : make_float4(0, 0, 0, 0);
-      x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) x[j] = expert(j) < E ? __ldg(row + expert(j)) : 0.f;
-  }
   const bool by_logit = a.softmax && !a.bias && !(GROUPS && a.top2);
-  float m = -INFINITY, inv = 1.f;
-  if (a.softmax) {
+  const bool rough = !GROUPS && !a.softmax;  // approximate keys find the candidates
+  const bool direct = !GROUPS && by_logit;
+  uint32_t key[NJ];
+  float m = -INFINITY;
+  {
+    float x[NJ], b[NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      if (expert(j) < E) m = fmaxf(m, x[j]);  // (ignores NaN)
-    m = warp_max(m);
-    if (!by_logit || !a.renorm) {
-      float sum = 0.f;
+    for (int j = 0; j < NJ; j += VEC ? 4 : 1) {
+      const bool in = expert(j) < E;
+      if constexpr (VEC) {
+        const float4 v = in ? __ldg(reinterpret_cast<const float4*>(row + expert(j))) : make_float4(0, 0, 0, 0);
+        const float4 w = in && a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + expert(j))) : make_float4(0, 0, 0, 0);
+        x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+        b[j] = w.x, b[j + 1] = w.y, b[j + 2] = w.z, b[j + 3] = w.w;
+      } else {
+        x[j] = in ? __ldg(row + expert(j)) : 0.f;
+        b[j] = in && a.bias ? __ldg(a.bias + expert(j)) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; j += VEC ? 4 : 1) {
+      if constexpr (VEC) {
+        *reinterpret_cast<float4*>(xs + expert(j)) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        *reinterpret_cast<float4*>(keys + expert(j)) = make_float4(b[j], b[j + 1], b[j + 2], b[j + 3]);
+      } else {
+        xs[expert(j)] = x[j];
+        keys[expert(j)] = __float_as_uint(b[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < (VEC ? 4 : 1); ++i)
+        if (expert(j + i) < E) m = fmaxf(m, x[j + i]);  // (ignores NaN)
+    }
+    if (rough) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
-        if (expert(j) < E) sum = __fadd_rn(sum, soft_exp(x[j], m));
+        key[j] = expert(j) < E ? order_key(__fadd_rn(topk_impl::approx_sigmoid(x[j]), b[j])) : 0u;
+    } else if (direct) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) key[j] = expert(j) < E ? order_key(number(x[j])) : 0u;
+    }
+  }
+  // (a lane reads back what it wrote until the next warp barrier)
+  float inv = 1.f;
+  const bool summed = a.softmax && (!by_logit || !a.renorm);  // xs then holds exp(x - max), NaN a NaN
+  if (a.softmax) {
+    m = warp_max(m);
+    if (summed) {
+      float sum = 0.f;
+#pragma unroll 1
+      for (int j0 = 0; j0 < NJ; j0 += 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = expert(j0 + i);
+          const float v = xs[e], x = soft_exp(v, m);
+          if (e < E) sum = __fadd_rn(sum, x);
+          if (!by_logit) xs[e] = v != v ? v : x;
+        }
       sum = warp_sum(sum);
       inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
     }
   }
-  auto score = [&](float v) {
-    if (a.softmax) return __fmul_rn(soft_exp(v, m), inv);
+  auto score = [&](float v) {  // of what xs holds
+    if (a.softmax) return __fmul_rn(by_logit ? soft_exp(v, m) : v != v ? 0.f : v, inv);
     return v != v ? 0.f : spec_sigmoid(v);
   };
-  // 1) keys
-  if (by_logit) {
+  auto exact_key = [&](float v, float bias) {
+    float c = v;
+    if (!by_logit) c = a.bias ? __fadd_rn(score(v), bias) : score(v);
+    return order_key(v != v ? -INFINITY : number(c));
+  };
+  // 1) exact keys of all experts
+  auto exact_keys = [&] {
+#pragma unroll 1
+    for (int j0 = 0; j0 < NJ; j0 += 4) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) key[j] = expert(j) < E ? order_key(number(x[j])) : 0u;
-  } else {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      float c = score(x[j]);
-      if (a.bias && expert(j) < E) c = __fadd_rn(c, __ldg(a.bias + expert(j)));
-      key[j] = expert(j) < E ? order_key(x[j] != x[j] ? -INFINITY : number(c)) : 0u;
+      for (int i = 0; i < 4; ++i) {
+        const int e = expert(j0 + i);
+        keys[e] = e < E ? exact_key(xs[e], __uint_as_float(keys[e])) : 0u;
+      }
     }
-  }
+#pragma unroll
+    for (int j = 0; j < NJ; j += VEC ? 4 : 1) {
+      if constexpr (VEC) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + expert(j));
+        key[j] = k.x, key[j + 1] = k.y, key[j + 2] = k.z, key[j + 3] = k.w;
+      } else {
+        key[j] = keys[expert(j)];
+      }
+    }
+  };
+  if (!rough && !direct) exact_keys();
   // 2) groups: L lanes each (of a power of two), the two largest keys of a group in each
   if constexpr (GROUPS) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      if (expert(j) < E) keys[expert(j)] = key[j];
     __syncwarp();
     const int size = E / a.n_group, L = 1 << (31 - __clz(32 / a.n_group)), g = lane / L, r = lane - g * L;
     const int steps = (size + L - 1) / L;
@@ -188,7 +237,9 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
     bound = __reduce_max_sync(kFull, v);
     v = v == bound ? 0u : v;
   }
-  bound = max(bound, 1u);
+  // (K experts have an approximate key of at least it: the exact K-th largest is within the
+  // approximation's error of it, and every expert chosen within twice that)
+  bound = rough ? topk_impl::candidate_threshold(bound) : max(bound, 1u);
   // 4) candidates, compacted
   int mine = 0;
 #pragma unroll
@@ -206,11 +257,17 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
     for (int j = 0; j < NJ; ++j) {
       if (key[j] >= bound) {
         ws.list[pos] = rank_key(key[j], expert(j));
-        ws.x[pos] = x[j];
         ++pos;
       }
     }
     __syncwarp();
+    if (rough) {  // the candidates' exact keys
+      for (int i = lane; i < total; i += 32) {
+        const int e = (int)(0xFFFFFFFFu - (uint32_t)ws.list[i]);
+        ws.list[i] = rank_key(exact_key(xs[e], __uint_as_float(keys[e])), e);
+      }
+      __syncwarp();
+    }
     // 5) a candidate's slot: how many order before it (lane i: candidates i and i + 32)
     auto place = [&](int i) {
       const unsigned long long c = i < total ? ws.list[i] : 0;
@@ -218,26 +275,28 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
 #pragma unroll 4
       for (int o = 0; o < total; ++o) r += ws.list[o] > c;
       if (i < total && r < K) {
-        ws.id[r] = (int)(0xFFFFFFFFu - (uint32_t)c);
-        ws.s[r] = score(ws.x[i]);
+        const int e = (int)(0xFFFFFFFFu - (uint32_t)c);
+        ws.id[r] = e;
+        ws.s[r] = score(xs[e]);
       }
     };
     place(lane);
     if (total > 32) place(lane + 32);
   } else {
+    if (rough) exact_keys();
+    __syncwarp();
 #pragma unroll 1
     for (int k = 0; k < K; ++k) {
       uint32_t best = 0;
       int at = 0x7FFFFFFF;
-      float bx = 0.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
-        if (key[j] > best) best = key[j], at = expert(j), bx = x[j];  // (ascending: the first maximum wins)
+        if (key[j] > best) best = key[j], at = expert(j);  // (ascending: the first maximum wins)
       const uint32_t top = __reduce_max_sync(kFull, best);
       const int win = (int)__reduce_min_sync(kFull, best == top ? (uint32_t)at : 0x7FFFFFFFu);
       if (at == win) {
         ws.id[k] = win;
-        ws.s[k] = score(bx);
+        ws.s[k] = score(xs[win]);
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
@@ -251,12 +310,13 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
 template <int NJ, bool VEC, bool GROUPS>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(const GroupedArgs a) {
   __shared__ RouteScratch ws[kWarps];
-  __shared__ uint32_t keys[GROUPS ? kWarps * NJ * 32 : 1];
+  __shared__ __align__(16) float xs[kWarps * NJ * 32];
+  __shared__ __align__(16) uint32_t keys[kWarps * NJ * 32];
   const int warp = threadIdx.x >> 5, t = blockIdx.x * kWarps + warp;
   grid_launch_dependents();
   if (t < a.T && (threadIdx.x & 31) == 0 && VEC) prefetch_l2(a.logits + (size_t)t * a.E, (uint32_t)a.E * 4u);  // (a hint)
   grid_wait();
-  if (t < a.T) route_token<NJ, VEC, GROUPS>(a, t, ws[warp], keys + (GROUPS ? warp * NJ * 32 : 0));
+  if (t < a.T) route_token<NJ, VEC, GROUPS>(a, t, ws[warp], xs + warp * NJ * 32, keys + warp * NJ * 32);
 }
 
 template <bool SOFTMAX, bool TOP2>
@@ -354,7 +414,7 @@ size_t one_wave_pad(long long blocks, size_t fixed, const DeviceInfo& dev) {
 template <int NJ, bool VEC, bool GROUPS>
 int launch_registers(const GroupedArgs& a, const DeviceInfo& dev, cudaStream_t s) {
   const unsigned blocks = (unsigned)((a.T + kWarps - 1) / kWarps);
-  const size_t fixed = kWarps * (sizeof(RouteScratch) + (GROUPS ? NJ * 32 * sizeof(uint32_t) : 0));
+  const size_t fixed = kWarps * (sizeof(RouteScratch) + 2 * NJ * 32 * sizeof(uint32_t));
   return launch_pdl(route_kernel<NJ, VEC, GROUPS>, dim3(blocks), dim3(32 * kWarps), one_wave_pad(blocks, fixed, dev), s, a);
 }
 

@@ -97,6 +97,18 @@ def test_ties_go_to_the_lowest_index(moe):
         check(moe, x, None, 32, scoring=scoring)
 
 
+@pytest.mark.parametrize("E", [300, 896, 1024])
+def test_more_ties_than_candidates(moe, E):
+    """More experts at the bound than are ranked against each other: the lowest indices, in order."""
+    x = np.zeros((3, E))
+    x[1, 100:] = 1.0
+    x[2, 200:205] = 3.0
+    for scoring in ("sigmoid", "softmax"):
+        check(moe, x, None, 16, scoring=scoring)
+        check(moe, x, np.zeros(E), 16, scoring=scoring)
+        check(moe, x, None, 16, scoring=scoring, groups=4, kept=2, rule="top2")
+
+
 def test_masked_and_special_logits(moe):
     """Rows whose mask leaves few, one or no experts (-inf or the type's lowest value), NaN, +inf."""
     low = float(np.finfo(np.float32).min)
