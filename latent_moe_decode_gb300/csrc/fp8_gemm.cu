@@ -19,10 +19,15 @@ int check(const GemmArgs& a, int out_dtype) {
 }
 
 // The kernel: 0 for the wide one, else the narrow one's rows a tile.
-// Grouped, by the lists' average length: wide from 96 on (64 experts, N = 4096, K = 3584: 64
-// rows 177 us narrow and 193 wide, 96 rows 220 and 198); below, a tile for the rows of all but
-// the fullest experts, half as many again as the average and four (256 experts of 9 rows: 88
-// us with 32, 94 with 16; 64 experts of 8: 145 with 16, 146 with 32).
+// Grouped, by the lists' average length, for tiles that hold all but the fullest lists. Times
+// in us of 256 experts of 1024 x 1024 / 64 of 4096 x 3584, the rows copied first from 32 on:
+//   average    16 rows     32 rows     64 rows      wide
+//         8    46 / 145    47 / 146    58 / 153    78 / 188
+//        16    54 / 154    53 / 155    63 / 156    82 / 190
+//        32    78 / 218    61 / 164    72 / 160    89 / 192
+//        48   104 / 307    76 / 198    85 / 172    88 / 194
+//        64   131 / 395    94 / 246    99 / 184    91 / 196
+//        80   159 / 479   110 / 288   113 / 208    94 / 198
 // Dense, up to 64 rows: the narrowest tile that holds them. Above, whatever is estimated to
 // end first: 0.43 us for a block of a wide tile and 4 us for the rest; 0.35 for a block of a
 // 64-row tile alone on an SM, 0.4 a CTA for two, and 3.5; 0.43 for one of a 128-row tile,
@@ -31,9 +36,8 @@ int check(const GemmArgs& a, int out_dtype) {
 // 7184 against 18 by 64 rows, the sum of 128 KB of partials a CTA and clusters of four or
 // eight whole SMs costing more than the blocks saved.)
 int choose_listed(int n_pairs, int E) {
-  if (n_pairs >= 96LL * E) return 0;
-  const long long want = (3LL * n_pairs / 2 + E - 1) / E + 4;
-  return want <= 16 ? 16 : want <= 32 ? 32 : 64;
+  if (n_pairs > 72LL * E) return 0;
+  return n_pairs > 40LL * E ? 64 : n_pairs > 10LL * E ? 32 : 16;
 }
 int choose(const GemmArgs& a, int sm_count) {
   if (a.offsets) return choose_listed(a.M, a.E);
@@ -51,13 +55,14 @@ int choose(const GemmArgs& a, int sm_count) {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Whether rows that do not lie in list order are copied there before the product: always for
-// the wide kernel, which reads boxes of them; for the narrow one, whose warp fetches single
-// rows at 16 a tile as fast as HBM brings the weights, and at 32 not quite (1020 tokens x 16
-// of 896 experts, N = 3584, K = 1024: 546 us, 505 with the copies), from where that costs
-// more than the copies' launch: some 50 us of weights.
-bool copies(int n_pairs, int E, int N, int K, int in_rows) {
+// the wide kernel, which reads boxes of them. The narrow one has a warp that looks up a tile's
+// rows and fetches them singly, at 16 a tile as fast as HBM brings the weights. At 32 that
+// costs more than the copies' launch from some hundred fetches an SM on (64 experts of 32 rows,
+// N = 1280, K = 512, 20480 fetches: 25.6 us, 21.6 with the copies; of 16 rows, 10240 fetches:
+// 34 and 38 at K = 2048); at 64, always (48 rows of 256 experts: 129 and 85; of 32: 24 and 25).
+bool copies(int n_pairs, int E, int N, int in_rows) {
   const int bn = choose_listed(n_pairs, E);
-  return in_rows != MOE_ROWS_LIST && (bn == 0 || (bn > 16 && (double)E * N * K > 256e6));
+  return in_rows != MOE_ROWS_LIST && (bn == 0 || bn == 64 || (bn == 32 && (long long)n_pairs * ((N - 1) / FP8_BLOCK + 1) > 16000));
 }
 
 // Copies of the listed pairs' rows and scales in list order.
@@ -104,7 +109,7 @@ int launch(GemmArgs& a, void* workspace, cudaStream_t stream) {
   long long rows = a.a_rows;
   const int bn = choose(a, dev.sm_count);
   bool named = a.offsets && a.in_rows != MOE_ROWS_LIST;
-  if (a.offsets && copies(a.M, a.E, a.N, a.K, a.in_rows)) {
+  if (a.offsets && copies(a.M, a.E, a.N, a.in_rows)) {
     uint8_t* copy = static_cast<uint8_t*>(workspace);
     float* scales = reinterpret_cast<float*>(copy + align256((size_t)a.M * a.K));
     const long long need = ((long long)a.M * 32 + kCopyThreads - 1) / kCopyThreads, most = 8LL * dev.sm_count;
@@ -130,7 +135,7 @@ extern "C" int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uin
 }
 
 extern "C" size_t moe_expert_gemm_workspace(int n_pairs, int E, int N, int K, int in_rows) {
-  if (n_pairs < 1 || E < 1 || N < 1 || K < 16 || !moe::copies(n_pairs, E, N, K, in_rows)) return 0;
+  if (n_pairs < 1 || E < 1 || N < 1 || K < 16 || !moe::copies(n_pairs, E, N, in_rows)) return 0;
   return moe::list_copy_bytes(n_pairs, K);
 }
 

@@ -344,9 +344,9 @@ def test_expert_gemm_bad_offsets(moe):
 
 
 @pytest.mark.parametrize("in_rows", ["ROWS_TOKEN", "ROWS_PAIR"])
-def test_expert_rows_copied_for_many_weights(moe, in_rows):
-    """Lists of some ten rows over more than 256 MB of weights: rows are copied to list order first."""
-    T, topk, E, N, K = 330, 2, 65, 1040, 4096
+@pytest.mark.parametrize("T,topk,E,N,K,copied", [(330, 2, 65, 1040, 4096, False), (700, 3, 65, 1040, 272, True), (350, 8, 65, 72, 400, True)])
+def test_expert_rows_fetched_or_copied(moe, in_rows, T, topk, E, N, K, copied):
+    """Lists of ten rows, fetched singly; of thirty for many columns, and of over forty: copied to list order first."""
     rng = np.random.default_rng(5)
     ids = np.stack([rng.permutation(E)[:topk] for _ in range(T)])
     rows = T if in_rows == "ROWS_TOKEN" else T * topk
@@ -355,7 +355,7 @@ def test_expert_rows_copied_for_many_weights(moe, in_rows):
     w = torch.randint(0, 0x78, (E, N, K), dtype=torch.uint8, device="cuda", generator=g)
     sw = torch.full((E, ref.nb(N), ref.nb(K)), 0.001, device="cuda")
     offsets, pairs = lists(ids, E)
-    assert moe.expert_gemm_workspace(T * topk, E, N, K, getattr(moe, in_rows)) > 0
+    assert (moe.expert_gemm_workspace(T * topk, E, N, K, getattr(moe, in_rows)) > 0) == copied
     out = moe.expert_gemm(dev(a), dev(sa), w, sw, dev(offsets), dev(pairs), topk, in_rows=getattr(moe, in_rows), out_dtype=torch.float32)
     for e in (0, 31, 64):
         p = pairs[offsets[e]:offsets[e + 1]]
