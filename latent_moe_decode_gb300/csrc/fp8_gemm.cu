@@ -29,11 +29,13 @@ int check(const GemmArgs& a, int out_dtype) {
 //        64   131 / 395    94 / 246    99 / 184    91 / 196
 //        80   159 / 479   110 / 288   113 / 208    94 / 198
 // Dense, up to 64 rows: the narrowest tile that holds them. Above, whatever is estimated to
-// end first: 0.43 us for a block of a wide tile and 4 us for the rest; 0.35 for a block of a
-// 64-row tile alone on an SM, 0.4 a CTA for two, and 3.5; 0.43 for one of a 128-row tile,
-// and 4 (5.5 where CTAs share a tile). (Splitting K over pairs of a wide tile, too,
-// measured slower: 15 us for 128 x 7168 x 3584 against 14.9 unsplit, 29 for 333 x 2016 x
-// 7184 against 18 by 64 rows, the sum of 128 KB of partials a CTA and clusters of four or
+// end first, in ns for w tiles one after the other (per SM, for the wide kernel per pair) of b
+// blocks each (of its split): wide 2700 + w (2250 + 350 b); 64 rows 5200 + w (2000 + 225 b),
+// split 7300 + 440 b; 128 rows w (5400 + 305 b), split 6700 + 360 b. (Fitted to 70 sizes, M
+// 128 to 2304, N 576 to 7168, K 400 to 7168, within 15 % of most; us wide / 64 / 128: 1024 x
+// 1024 x 400 6.5 / 9.0 / 8.3, x 3584 14.4 / 13.7 / 11.9; 2304 x 2304 x 1296 15.3 / 26.6 /
+// 27.5. Splitting K over pairs of a wide tile, too, measured slower: 15 us for 128 x 7168 x
+// 3584, 29 for 333 x 2016 x 7184, the sum of 128 KB of partials a CTA and clusters of four or
 // eight whole SMs costing more than the blocks saved.)
 int choose_listed(int n_pairs, int E) {
   if (n_pairs > 72LL * E) return 0;
@@ -43,11 +45,12 @@ int choose(const GemmArgs& a, int sm_count) {
   if (a.offsets) return choose_listed(a.M, a.E);
   if (a.M <= 64) return a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64;
   const long long M = a.M, tiles0 = ((M - 1) / 256 + 1) * ((a.nbn + 1) / 2), pairs = sm_count / 2;
-  const long long ns0 = 4000 + ((tiles0 - 1) / pairs + 1) * a.nbk * 430;
+  const long long w0 = (tiles0 - 1) / pairs + 1, ns0 = 2700 + w0 * (2250 + a.nbk * 350);
   const long long tiles64 = ((M - 1) / 64 + 1) * a.nbn, tiles128 = ((M - 1) / 128 + 1) * a.nbn;
   const int s64 = fp8_impl::narrow_splits(64, tiles64, a.nbk, sm_count), s128 = fp8_impl::narrow_splits(128, tiles128, a.nbk, sm_count);
-  const long long ns64 = 3500 + ((tiles64 * s64 - 1) / sm_count + 1) * ((a.nbk - 1) / s64 + 1) * (s64 > 1 ? 400 : 350);
-  const long long ns128 = (s128 > 1 ? 5500 : 4000) + ((tiles128 * s128 - 1) / sm_count + 1) * ((a.nbk - 1) / s128 + 1) * 430;
+  const long long w64 = (tiles64 - 1) / sm_count + 1, w128 = (tiles128 - 1) / sm_count + 1;
+  const long long ns64 = s64 > 1 ? 7300 + ((a.nbk - 1) / s64 + 1) * 440 : 5200 + w64 * (2000 + a.nbk * 225);
+  const long long ns128 = s128 > 1 ? 6700 + ((a.nbk - 1) / s128 + 1) * 360 : w128 * (5400 + a.nbk * 305);
   if (ns0 <= ns64 && ns0 <= ns128) return 0;
   return ns64 <= ns128 ? 64 : 128;
 }

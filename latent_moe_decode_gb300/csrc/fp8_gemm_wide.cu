@@ -103,12 +103,12 @@ __device__ __forceinline__ void transpose4(uint32_t (&u)[4][8]) {
   }
 }
 
-// The warp's 64 columns from n on of its 32 rows (`row` this lane's, -1: none). With whole,
-// 32-byte aligned pieces (vec) four lanes exchange theirs first, so that a store covers 128
-// contiguous bytes of eight rows and not 32 of all 32 (those took an eighth of the time of
-// 4096 x 7168 x 3584); else by way of the warp's pad in shared memory, 16 columns of two rows
-// a store (one value of 32 rows a store took 45 us for 500 x 1000 x 3008).
-__device__ __forceinline__ void store_rows(const GemmArgs& g, long long row, int n, const float (&acc)[64], bool vec,
+// The warp's 64 columns from n on of its 32 rows (`row` this lane's, -1: none). Where rows
+// start at multiples of 32 or 16 bytes (vec) four lanes exchange their pieces first, so that
+// a store covers 128 contiguous bytes of eight rows and not 32 of all 32 (those took an eighth
+// of the time of 4096 x 7168 x 3584); else by way of the warp's pad in shared memory, 16
+// columns of two rows a store (one value of 32 rows a store took 45 us for 500 x 1000 x 3008).
+__device__ __forceinline__ void store_rows(const GemmArgs& g, long long row, int n, const float (&acc)[64], int vec,
                                            float (*pad)[kPadCols + 1]) {
   const int lane = threadIdx.x & 31;
   if (vec) {
@@ -118,7 +118,15 @@ __device__ __forceinline__ void store_rows(const GemmArgs& g, long long row, int
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const long long r = __shfl_sync(kFullMask, row, (lane & ~3) + i);
-        if (r >= 0) st32(static_cast<uint8_t*>(g.out) + (r * g.N + at) * size + 32 * (lane & 3), u[i]);
+        const int c = at + 32 / size * (lane & 3);
+        uint8_t* const to = static_cast<uint8_t*>(g.out) + (r * g.N + c) * size;
+        if (r < 0) continue;
+        if (vec == 32 && at + 128 / size <= g.N) {
+          st32(to, u[i]);
+        } else {
+          if (c < g.N) *reinterpret_cast<uint4*>(to) = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
+          if (c + 16 / size < g.N) *reinterpret_cast<uint4*>(to + 16) = make_uint4(u[i][4], u[i][5], u[i][6], u[i][7]);
+        }
       }
     };
     if (g.f32) {
@@ -364,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (kb + 1 < g.nbk && ok) fold(1);
       }
       if (!ok) break;
-      if (n < g.N) store_rows(g, out, n, acc, vec && n + 64 <= g.N, pads[warp]);
+      if (n < g.N) store_rows(g, out, n, acc, vec, pads[warp]);
       __syncwarp();
     }
   }
@@ -391,7 +399,8 @@ int launch(const GemmArgs& g, long long a_rows, int sm_count, cudaStream_t strea
   static OncePerDevice once;
   if (!once.allow(reinterpret_cast<const void*>(kern), (int)smem)) return MOE_ERR_CUDA;
   const size_t esize = g.f32 ? 4 : 2;
-  const int vec = aligned(g.out, 32) && ((size_t)g.N * esize) % 32 == 0;
+  const size_t row_bytes = g.N * esize;
+  const int vec = aligned(g.out, 32) && row_bytes % 32 == 0 ? 32 : aligned(g.out, 16) && row_bytes % 16 == 0 ? 16 : 0;
   const int pairs = sm_count / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)(tiles < pairs ? tiles : pairs));
