@@ -183,15 +183,15 @@ __global__ void __launch_bounds__(kMaxThreads<V>) block_norm_kernel(const BlockN
       float w[8];
       bf16x8_to_f32(next[i], w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(r[i][j], w[j]);  // n = w * root
+      for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(__fmul_rn(r[i][j], root), w[j]);  // n
       if (a.n && f < nv)
-        st16(a.n + at + 8 * f,
-             make_uint4(pack_bf16x2(__fmul_rn(w[0], root), __fmul_rn(w[1], root)), pack_bf16x2(__fmul_rn(w[2], root), __fmul_rn(w[3], root)),
-                        pack_bf16x2(__fmul_rn(w[4], root), __fmul_rn(w[5], root)), pack_bf16x2(__fmul_rn(w[6], root), __fmul_rn(w[7], root))));
+        st16(a.n + at + 8 * f, make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])));
       if (a.q) {
-        // n / amax(n) = w / amax(w): the codes need neither the root nor its rounding
-        const float top = __uint_as_float(block_max(magnitude(w)));
-        const BlockScale s = block_scale_of_product(top, root);
+        // (Of n, not of h * weight, whose ratios are the same: its multipliers can overflow where n's
+        // cannot, and it is not zero where a root of 0 makes n so. Lanes past the row's end hold 0, or
+        // NaN where an infinite root makes the rest of their block infinite or NaN. 73.4 us at 4096 x
+        // 7168, 72.9 with the codes of h * weight.)
+        const BlockScale s = block_scale_shared(block_max(magnitude(w)));
         if (f < nv) {
           *reinterpret_cast<uint2*>(a.q + at + 8 * f) = encode8(w, s);
           if ((f & 15) == 0) a.scales[row * a.nb + (f >> 4)] = s.scale;

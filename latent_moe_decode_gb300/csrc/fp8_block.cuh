@@ -45,20 +45,16 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t m) {
   return s;
 }
 
-// The same (amax / 448) of values v * f, f > 0 common to the block, whose largest |v| is
-// `top`: the scale is that of the products, mult the multiplier of v. With the warp's lanes
-// in step and a block's lanes agreeing on top: even lanes divide for the scale, odd lanes for
-// the multiplier.
-__device__ __forceinline__ BlockScale block_scale_of_product(float top, float f) {
+// The same (amax / 448), the warp's lanes in step and a block's lanes agreeing on m: even lanes
+// divide for the scale, odd lanes for the multiplier.
+__device__ __forceinline__ BlockScale block_scale_shared(uint32_t m) {
   BlockScale s;
-  const float amax = __fmul_rn(top, f);
-  s.special = !(amax < __uint_as_float(kInf));  // (NaN too)
-  const bool tiny = amax < __uint_as_float(kTiny), odd = threadIdx.x & 1;
-  const float used = s.special ? 1.f : fmaxf(amax, __uint_as_float(kTiny));
-  const float over = s.special ? 1.f : tiny ? used : top;
-  const float d = __fdiv_rn(odd ? 448.f : used, odd ? over : 448.f), o = __shfl_xor_sync(kFullMask, d, 1);
-  s.scale = s.special ? __uint_as_float(0x7FC00000u) : amax == 0.f ? 1.f : odd ? o : d;
-  s.mult = amax == 0.f ? 1.f : tiny ? __fmul_rn(odd ? d : o, f) : odd ? d : o;
+  s.special = m >= kInf;
+  const bool odd = threadIdx.x & 1;
+  const float used = __uint_as_float(s.special ? kTiny : max(m, kTiny));
+  const float d = __fdiv_rn(odd ? 448.f : used, odd ? used : 448.f), o = __shfl_xor_sync(kFullMask, d, 1);
+  s.scale = s.special ? __uint_as_float(0x7FC00000u) : m == 0u ? 1.f : odd ? o : d;
+  s.mult = m == 0u ? 1.f : odd ? d : o;
   return s;
 }
 
