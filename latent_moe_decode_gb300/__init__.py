@@ -135,7 +135,17 @@ def _need(t, dtype, shape=None, name="tensor"):
     raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _empty(shape, dtype, like):
+def _empty(shape, dtype, like, stream=None):
+    """A new tensor for a launch on `stream`: of that stream's memory, so that it is neither still in
+    use by the current stream's earlier work nor, once dropped, handed to its later work while the
+    launch runs; the current stream may use it as well."""
+    if stream is not None:
+        current = torch.cuda.current_stream(like.device)
+        if stream.cuda_stream != current.cuda_stream:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream.cuda_stream, device=like.device)):
+                t = torch.empty(shape, dtype=dtype, device=like.device)
+            t.record_stream(current)
+            return t
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
@@ -150,10 +160,10 @@ def router_logits(x, w, out=None, workspace=None, algo: int = ROUTER_AUTO, strea
     E = w.shape[0]
     _need(x, torch.bfloat16, (T, H), "x")
     _need(w, torch.bfloat16, (E, H), "w")
-    out = _empty((T, E), torch.float32, x) if out is None else _need(out, torch.float32, (T, E), "out")
+    out = _empty((T, E), torch.float32, x, stream) if out is None else _need(out, torch.float32, (T, E), "out")
     need = router_logits_workspace(T, H, E)
     if need and workspace is None:
-        workspace = _empty((need,), torch.uint8, x)
+        workspace = _empty((need,), torch.uint8, x, stream)
     wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("moe_router_logits_ex", load().moe_router_logits_ex(
         _ptr(x), _ptr(w), _ptr(out), T, H, E, _ptr(workspace), wb, algo, _stream(stream)))
@@ -171,11 +181,11 @@ def front_projection(x, w_router, w_down, logits=None, latent=None, workspace=No
     _need(x, torch.bfloat16, (T, H), "x")
     _need(w_router, torch.bfloat16, (E, H), "w_router")
     _need(w_down, torch.bfloat16, (L, H), "w_down")
-    logits = _empty((T, E), torch.float32, x) if logits is None else _need(logits, torch.float32, (T, E), "logits")
-    latent = _empty((T, L), torch.bfloat16, x) if latent is None else _need(latent, torch.bfloat16, (T, L), "latent")
+    logits = _empty((T, E), torch.float32, x, stream) if logits is None else _need(logits, torch.float32, (T, E), "logits")
+    latent = _empty((T, L), torch.bfloat16, x, stream) if latent is None else _need(latent, torch.bfloat16, (T, L), "latent")
     need = front_projection_workspace(T, H, E, L)
     if need and workspace is None:
-        workspace = _empty((need,), torch.uint8, x)
+        workspace = _empty((need,), torch.uint8, x, stream)
     wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("moe_front_projection", load().moe_front_projection(
         _ptr(x), _ptr(w_router), _ptr(w_down), _ptr(logits), _ptr(latent), T, H, E, L, _ptr(workspace), wb,
@@ -190,10 +200,10 @@ def topk_route(logits, bias, K: int, renormalize: bool = True, scale: float = 1.
     _need(logits, torch.float32, (T, E), "logits")
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
-    ids = _empty((T, K), torch.int32, logits) if ids is None else _need(ids, torch.int32, (T, K), "ids")
-    weights = _empty((T, K), torch.float32, logits) if weights is None else _need(weights, torch.float32, (T, K), "weights")
+    ids = _empty((T, K), torch.int32, logits, stream) if ids is None else _need(ids, torch.int32, (T, K), "ids")
+    weights = _empty((T, K), torch.float32, logits, stream) if weights is None else _need(weights, torch.float32, (T, K), "weights")
     if weights_bf16 is None and want_bf16:
-        weights_bf16 = _empty((T, K), torch.bfloat16, logits)
+        weights_bf16 = _empty((T, K), torch.bfloat16, logits, stream)
     elif weights_bf16 is not None:
         _need(weights_bf16, torch.bfloat16, (T, K), "weights_bf16")
     _check("moe_topk_route", load().moe_topk_route(
@@ -212,11 +222,11 @@ def topk_route_quantize(logits, bias, K: int, latent, renormalize: bool = True, 
         _need(bias, torch.float32, (E,), "bias")
     rows, cols = latent.shape
     _need(latent, torch.bfloat16, (rows, cols), "latent")
-    ids = _empty((T, K), torch.int32, logits) if ids is None else _need(ids, torch.int32, (T, K), "ids")
-    weights = _empty((T, K), torch.float32, logits) if weights is None else _need(weights, torch.float32, (T, K), "weights")
-    weights_bf16 = _empty((T, K), torch.bfloat16, logits) if weights_bf16 is None else _need(weights_bf16, torch.bfloat16, (T, K), "weights_bf16")
-    q = _empty((rows, cols), torch.uint8, latent) if q is None else _need(q, torch.uint8, (rows, cols), "q")
-    scales = _empty((rows, cols // 32), torch.uint8, latent) if scales is None else _need(scales, torch.uint8, (rows, cols // 32), "scales")
+    ids = _empty((T, K), torch.int32, logits, stream) if ids is None else _need(ids, torch.int32, (T, K), "ids")
+    weights = _empty((T, K), torch.float32, logits, stream) if weights is None else _need(weights, torch.float32, (T, K), "weights")
+    weights_bf16 = _empty((T, K), torch.bfloat16, logits, stream) if weights_bf16 is None else _need(weights_bf16, torch.bfloat16, (T, K), "weights_bf16")
+    q = _empty((rows, cols), torch.uint8, latent, stream) if q is None else _need(q, torch.uint8, (rows, cols), "q")
+    scales = _empty((rows, cols // 32), torch.uint8, latent, stream) if scales is None else _need(scales, torch.uint8, (rows, cols // 32), "scales")
     _check("moe_topk_route_quantize", load().moe_topk_route_quantize(
         _ptr(logits), _ptr(bias), T, E, K, int(bool(renormalize)), float(scale), _ptr(ids), _ptr(weights),
         _ptr(weights_bf16), _ptr(latent), rows, cols, _ptr(q), _ptr(scales), _stream(stream)))
@@ -231,11 +241,11 @@ def build_routing_lists(ids, E: int, offsets=None, pairs=None, workspace=None, s
     """CSR lists: offsets int32 [E+1], pairs int32 [T*K] (pair code t*K + k)."""
     T, K = ids.shape
     _need(ids, torch.int32, (T, K), "ids")
-    offsets = _empty((E + 1,), torch.int32, ids) if offsets is None else _need(offsets, torch.int32, (E + 1,), "offsets")
-    pairs = _empty((T * K,), torch.int32, ids) if pairs is None else _need(pairs, torch.int32, (T * K,), "pairs")
+    offsets = _empty((E + 1,), torch.int32, ids, stream) if offsets is None else _need(offsets, torch.int32, (E + 1,), "offsets")
+    pairs = _empty((T * K,), torch.int32, ids, stream) if pairs is None else _need(pairs, torch.int32, (T * K,), "pairs")
     need = build_routing_lists_workspace(T, K, E)
     if need and workspace is None:
-        workspace = _empty((need,), torch.uint8, ids)
+        workspace = _empty((need,), torch.uint8, ids, stream)
     wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("moe_build_routing_lists", load().moe_build_routing_lists(
         _ptr(ids), T, K, E, _ptr(offsets), _ptr(pairs), _ptr(workspace), wb, _stream(stream)))
@@ -260,11 +270,11 @@ def unit_windows(offsets, window: int = 8, max_units: int | None = None, unit_of
         max_units = unit_expert.shape[0] if unit_expert is not None else None
     if max_units is None:
         raise ValueError("max_units (or preallocated unit arrays) required: see unit_windows_capacity()")
-    unit_offsets = _empty((E + 1,), torch.int32, offsets) if unit_offsets is None else _need(unit_offsets, torch.int32, (E + 1,), "unit_offsets")
+    unit_offsets = _empty((E + 1,), torch.int32, offsets, stream) if unit_offsets is None else _need(unit_offsets, torch.int32, (E + 1,), "unit_offsets")
     outs = []
     for t, name in ((unit_expert, "unit_expert"), (unit_start, "unit_start"), (unit_len, "unit_len")):
         if t is None:
-            t = _empty((max_units,), torch.int32, offsets)
+            t = _empty((max_units,), torch.int32, offsets, stream)
         elif _need(t, torch.int32, None, name).dim() != 1 or t.shape[0] < max_units:
             raise ValueError(f"{name}: expected a 1-D tensor of at least {max_units} entries")
         outs.append(t)
@@ -279,9 +289,9 @@ def mxfp8_quantize_rows(x, q=None, scales=None, stream=None, scale_rule: int = M
     scale_rule MXFP8_SCALE_FLOOR (OCP) or MXFP8_SCALE_CEIL (no saturation)."""
     rows, cols = x.shape
     _need(x, torch.bfloat16, (rows, cols), "x")
-    q = _empty((rows, cols), torch.uint8, x) if q is None else _need(q, torch.uint8, (rows, cols), "q")
+    q = _empty((rows, cols), torch.uint8, x, stream) if q is None else _need(q, torch.uint8, (rows, cols), "q")
     nb = cols // 32
-    scales = _empty((rows, nb), torch.uint8, x) if scales is None else _need(scales, torch.uint8, (rows, nb), "scales")
+    scales = _empty((rows, nb), torch.uint8, x, stream) if scales is None else _need(scales, torch.uint8, (rows, nb), "scales")
     _check("mxfp8_quantize_rows_ex", load().mxfp8_quantize_rows_ex(_ptr(x), rows, cols, _ptr(q), _ptr(scales),
                                                                    int(scale_rule), _stream(stream)))
     return q, scales
@@ -297,9 +307,9 @@ def mxfp8_quantize_rows_tcgen05(x, q=None, scales=None, stream=None, scale_rule:
     in the tcgen05 block-scaling tile layout)."""
     rows, cols = x.shape
     _need(x, torch.bfloat16, (rows, cols), "x")
-    q = _empty((rows, cols), torch.uint8, x) if q is None else _need(q, torch.uint8, (rows, cols), "q")
+    q = _empty((rows, cols), torch.uint8, x, stream) if q is None else _need(q, torch.uint8, (rows, cols), "q")
     n = mxfp8_tcgen05_scales_bytes(rows, cols)
-    scales = _empty((n,), torch.uint8, x) if scales is None else _need(scales, torch.uint8, (n,), "scales")
+    scales = _empty((n,), torch.uint8, x, stream) if scales is None else _need(scales, torch.uint8, (n,), "scales")
     _check("mxfp8_quantize_rows_tcgen05", load().mxfp8_quantize_rows_tcgen05(
         _ptr(x), rows, cols, _ptr(q), _ptr(scales), int(scale_rule), _stream(stream)))
     return q, scales
@@ -320,7 +330,7 @@ def finalize(rows, weights, T: int, K: int, row_index=None, shared=None, scale: 
         _need(row_index, torch.int32, (T, K), "row_index")
     if shared is not None:
         _need(shared, torch.bfloat16, (T, H), "shared")
-    out = _empty((T, H), torch.bfloat16, rows) if out is None else _need(out, torch.bfloat16, (T, H), "out")
+    out = _empty((T, H), torch.bfloat16, rows, stream) if out is None else _need(out, torch.bfloat16, (T, H), "out")
     _check("moe_finalize", load().moe_finalize(
         _ptr(rows), n_rows, _ptr(row_index), _ptr(weights), dt, _ptr(shared), float(scale), T, K, H, _ptr(out),
         _stream(stream)))
@@ -343,10 +353,10 @@ def finalize_rmsnorm(rows, weights, T: int, K: int, norm_weight, eps: float = 1e
     if row_index is not None:
         _need(row_index, torch.int32, (T, K), "row_index")
     if routed is None and want_routed:
-        routed = _empty((T, H), torch.bfloat16, rows)
+        routed = _empty((T, H), torch.bfloat16, rows, stream)
     elif routed is not None:
         _need(routed, torch.bfloat16, (T, H), "routed")
-    out = _empty((T, H), torch.bfloat16, rows) if out is None else _need(out, torch.bfloat16, (T, H), "out")
+    out = _empty((T, H), torch.bfloat16, rows, stream) if out is None else _need(out, torch.bfloat16, (T, H), "out")
     _check("moe_finalize_rmsnorm", load().moe_finalize_rmsnorm(
         _ptr(rows), n_rows, _ptr(row_index), _ptr(weights), dt, float(scale), _ptr(norm_weight), float(eps), T, K, H,
         _ptr(routed), _ptr(out), _stream(stream)))
@@ -435,12 +445,12 @@ def topk_route_grouped(logits, bias, K: int, n_group: int = 1, topk_group: int =
     _need(logits, torch.float32, (T, E), "logits")
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
-    ids = _empty((T, K), torch.int32, logits) if ids is None else _need(ids, torch.int32, (T, K), "ids")
-    weights = _empty((T, K), torch.float32, logits) if weights is None else _need(weights, torch.float32, (T, K), "weights")
+    ids = _empty((T, K), torch.int32, logits, stream) if ids is None else _need(ids, torch.int32, (T, K), "ids")
+    weights = _empty((T, K), torch.float32, logits, stream) if weights is None else _need(weights, torch.float32, (T, K), "weights")
     if weights_bf16 is not None:
         _need(weights_bf16, torch.bfloat16, (T, K), "weights_bf16")
     elif want_bf16:
-        weights_bf16 = _empty((T, K), torch.bfloat16, logits)
+        weights_bf16 = _empty((T, K), torch.bfloat16, logits, stream)
     _check("moe_topk_route_grouped", load().moe_topk_route_grouped(
         _ptr(logits), _ptr(bias), T, E, K, int(scoring), int(n_group), int(topk_group), int(group_rule),
         int(bool(renormalize)), float(scale), _ptr(ids), _ptr(weights), _ptr(weights_bf16), _stream(stream)))
@@ -449,9 +459,9 @@ def topk_route_grouped(logits, bias, K: int, n_group: int = 1, topk_group: int =
 
 def _block_quantize(fn, x, cols, q, scales, scale_rule, stream):
     rows = x.shape[0]
-    q = _empty((rows, cols), torch.uint8, x) if q is None else _need(q, torch.uint8, (rows, cols), "q")
+    q = _empty((rows, cols), torch.uint8, x, stream) if q is None else _need(q, torch.uint8, (rows, cols), "q")
     nb = _blocks(cols)
-    scales = _empty((rows, nb), torch.float32, x) if scales is None else _need(scales, torch.float32, (rows, nb), "scales")
+    scales = _empty((rows, nb), torch.float32, x, stream) if scales is None else _need(scales, torch.float32, (rows, nb), "scales")
     _check(fn, getattr(load(), fn)(_ptr(x), _row_stride(x), rows, cols, _ptr(q), _ptr(scales), int(scale_rule),
                                    _stream(stream)))
     return q, scales
@@ -482,7 +492,7 @@ def fp8_block_gemm(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16,
     _need(w, torch.uint8, (N, K), "w")
     _need(w_scales, torch.float32, (_blocks(N), _blocks(K)), "w_scales")
     dt, code = _out_dtype(out, out_dtype)
-    out = _empty((M, N), dt, a) if out is None else _need(out, dt, (M, N), "out")
+    out = _empty((M, N), dt, a, stream) if out is None else _need(out, dt, (M, N), "out")
     _check("fp8_block_gemm", load().fp8_block_gemm(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(out), code,
                                                    M, N, K, _stream(stream)))
     return out
@@ -508,10 +518,10 @@ def expert_gemm(a, a_scales, w, w_scales, offsets, pairs, topk: int, in_rows: in
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(pairs, torch.int32, (P,), "pairs")
     dt, code = _out_dtype(out, out_dtype)
-    out = _empty((P, N), dt, a) if out is None else _need(out, dt, (P, N), "out")
+    out = _empty((P, N), dt, a, stream) if out is None else _need(out, dt, (P, N), "out")
     need = expert_gemm_workspace(P, E, N, K, in_rows)
     if need and workspace is None:
-        workspace = _empty((need,), torch.uint8, a)
+        workspace = _empty((need,), torch.uint8, a, stream)
     wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("moe_expert_gemm", load().moe_expert_gemm(
         _ptr(a), _ptr(a_scales), a_rows, _ptr(w), _ptr(w_scales), _ptr(offsets), _ptr(pairs), P, int(topk), int(in_rows),
@@ -540,12 +550,12 @@ def block_norm(y, residual, next_weight, post_weight=None, gate=None, alpha: flo
         kind = {full: GATE_FULL, row: GATE_CHANNEL, (T, 1): GATE_TOKEN}.get(tuple(gate.shape))
         if kind is None:
             raise ValueError(f"gate: expected shape {(T, 1)}, {row} or {full}, got {tuple(gate.shape)}")
-    h = _empty((T, H), dt, y) if h is None else _need(h, dt, (T, H), "h")
-    n = _empty((T, H), torch.bfloat16, y) if n is None else _need(n, torch.bfloat16, (T, H), "n")
+    h = _empty((T, H), dt, y, stream) if h is None else _need(h, dt, (T, H), "h")
+    n = _empty((T, H), torch.bfloat16, y, stream) if n is None else _need(n, torch.bfloat16, (T, H), "n")
     if quantize:
-        q = _empty((T, H), torch.uint8, y) if q is None else _need(q, torch.uint8, (T, H), "q")
+        q = _empty((T, H), torch.uint8, y, stream) if q is None else _need(q, torch.uint8, (T, H), "q")
         nb = _blocks(H)
-        scales = _empty((T, nb), torch.float32, y) if scales is None else _need(scales, torch.float32, (T, nb), "scales")
+        scales = _empty((T, nb), torch.float32, y, stream) if scales is None else _need(scales, torch.float32, (T, nb), "scales")
     else:
         q = scales = None
     _check("moe_block_norm", load().moe_block_norm(
