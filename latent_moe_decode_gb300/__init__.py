@@ -149,6 +149,19 @@ def _empty(shape, dtype, like, stream=None):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _scratch(workspace, need, like, stream):
+    """(workspace, its bytes): the caller's, of any type and shape, or a new one of `need` bytes (None for 0)."""
+    if workspace is None:
+        return (_empty((need,), torch.uint8, like, stream), need) if need else (None, 0)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
+    if not workspace.is_cuda and workspace.numel():
+        raise ValueError("workspace: must be a CUDA tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 # ---------------------------------------------------------------------------
 def router_logits_workspace(T: int, H: int, E: int) -> int:
     return int(load().moe_router_logits_workspace(T, H, E))
@@ -161,10 +174,7 @@ def router_logits(x, w, out=None, workspace=None, algo: int = ROUTER_AUTO, strea
     _need(x, torch.bfloat16, (T, H), "x")
     _need(w, torch.bfloat16, (E, H), "w")
     out = _empty((T, E), torch.float32, x, stream) if out is None else _need(out, torch.float32, (T, E), "out")
-    need = router_logits_workspace(T, H, E)
-    if need and workspace is None:
-        workspace = _empty((need,), torch.uint8, x, stream)
-    wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wb = _scratch(workspace, router_logits_workspace(T, H, E), x, stream)
     _check("moe_router_logits_ex", load().moe_router_logits_ex(
         _ptr(x), _ptr(w), _ptr(out), T, H, E, _ptr(workspace), wb, algo, _stream(stream)))
     return out
@@ -183,10 +193,7 @@ def front_projection(x, w_router, w_down, logits=None, latent=None, workspace=No
     _need(w_down, torch.bfloat16, (L, H), "w_down")
     logits = _empty((T, E), torch.float32, x, stream) if logits is None else _need(logits, torch.float32, (T, E), "logits")
     latent = _empty((T, L), torch.bfloat16, x, stream) if latent is None else _need(latent, torch.bfloat16, (T, L), "latent")
-    need = front_projection_workspace(T, H, E, L)
-    if need and workspace is None:
-        workspace = _empty((need,), torch.uint8, x, stream)
-    wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wb = _scratch(workspace, front_projection_workspace(T, H, E, L), x, stream)
     _check("moe_front_projection", load().moe_front_projection(
         _ptr(x), _ptr(w_router), _ptr(w_down), _ptr(logits), _ptr(latent), T, H, E, L, _ptr(workspace), wb,
         _stream(stream)))
@@ -243,10 +250,7 @@ def build_routing_lists(ids, E: int, offsets=None, pairs=None, workspace=None, s
     _need(ids, torch.int32, (T, K), "ids")
     offsets = _empty((E + 1,), torch.int32, ids, stream) if offsets is None else _need(offsets, torch.int32, (E + 1,), "offsets")
     pairs = _empty((T * K,), torch.int32, ids, stream) if pairs is None else _need(pairs, torch.int32, (T * K,), "pairs")
-    need = build_routing_lists_workspace(T, K, E)
-    if need and workspace is None:
-        workspace = _empty((need,), torch.uint8, ids, stream)
-    wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wb = _scratch(workspace, build_routing_lists_workspace(T, K, E), ids, stream)
     _check("moe_build_routing_lists", load().moe_build_routing_lists(
         _ptr(ids), T, K, E, _ptr(offsets), _ptr(pairs), _ptr(workspace), wb, _stream(stream)))
     return offsets, pairs
@@ -395,7 +399,7 @@ def route_finalize(x, w, bias, latent, rows, K: int, renormalize: bool, scale: f
         _need(t, dt, shape, name)
     if weights is not None:
         _need(weights, torch.float32, (T, K), "weights")
-    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws = _scratch(workspace, 0, x, stream)
     _check("moe_route_finalize", load().moe_route_finalize(
         _ptr(x), _ptr(w), _ptr(bias), _ptr(latent), _ptr(rows), T, H, L, E, K, int(bool(renormalize)), float(scale),
         _ptr(logits), _ptr(ids), _ptr(weights), _ptr(weights_bf16), _ptr(offsets), _ptr(pairs), _ptr(q), _ptr(scales),
@@ -519,10 +523,7 @@ def expert_gemm(a, a_scales, w, w_scales, offsets, pairs, topk: int, in_rows: in
     _need(pairs, torch.int32, (P,), "pairs")
     dt, code = _out_dtype(out, out_dtype)
     out = _empty((P, N), dt, a, stream) if out is None else _need(out, dt, (P, N), "out")
-    need = expert_gemm_workspace(P, E, N, K, in_rows)
-    if need and workspace is None:
-        workspace = _empty((need,), torch.uint8, a, stream)
-    wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wb = _scratch(workspace, expert_gemm_workspace(P, E, N, K, in_rows), a, stream)
     _check("moe_expert_gemm", load().moe_expert_gemm(
         _ptr(a), _ptr(a_scales), a_rows, _ptr(w), _ptr(w_scales), _ptr(offsets), _ptr(pairs), P, int(topk), int(in_rows),
         int(out_rows), _ptr(out), code, E, N, K, _ptr(workspace), wb, _stream(stream)))
