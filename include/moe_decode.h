@@ -440,7 +440,10 @@ int moe_route_finalize(const uint16_t* x, const uint16_t* w, const float* bias, 
  * A NaN logit has score 0 and key -infinity (below every number, chosen last), as has a
  * NaN sum of score and bias its key; a logit of -infinity has score 0, and softmax over
  * no logit above -infinity gives scores of 0. Under softmax the logits of +infinity
- * share 1 equally.
+ * share 1 equally, and the others have score 0. Scores and keys are FP32, so that scores
+ * which FP32 does not tell apart tie; but softmax without a bias and without sums of keys
+ * (one group, all kept, or MOE_GROUP_MAX) goes by the order of the scores before their
+ * rounding.
  *
  *   logits       device, FP32 [T, E]
  *   bias         device, FP32 [E] or NULL

@@ -17,8 +17,8 @@
 //     (measured over all inputs, see topk.cuh) widens the bound; exact keys for the
 //     candidates alone.
 //   - Softmax without a bias and with groups by their maximum chooses by the logits, the
-//     order of the exact scores; its weights need the row's sum only when they are not
-//     renormalised (e / S over the sum of e / S).
+//     order of the scores before their rounding (logit_key); its weights need the row's sum only
+//     when they are not renormalised (e / S over the sum of e / S).
 // More than 1024 experts, or 32 groups, take a plainer body: the row in shared memory,
 // rounds over it for groups and choices.
 #include "topk.cuh"
@@ -60,6 +60,12 @@ __device__ __forceinline__ float number(float v) { return v != v ? -INFINITY : v
 __device__ __forceinline__ float soft_exp(float x, float m) {
   if (x != x || m == -INFINITY) return 0.f;
   return x == m ? 1.f : expf(x - m);
+}
+
+// Softmax's key by logit, m the row's maximum: where that is infinite every other number scores 0,
+// and ties; NaN lies below all (order_key).
+__device__ __forceinline__ uint32_t logit_key(float x, float m) {
+  return order_key(m == INFINITY && x < m ? 0.f : x);
 }
 
 // The weights of slots 0 .. K - 1 (lane k: slot k's expert and score).
@@ -170,8 +176,8 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
     return v != v ? 0.f : spec_sigmoid(v);
   };
   auto exact_key = [&](float v, float bias) {
-    float c = v;
-    if (!by_logit) c = a.bias ? __fadd_rn(score(v), bias) : score(v);
+    if (by_logit) return logit_key(v, m);
+    const float c = a.bias ? __fadd_rn(score(v), bias) : score(v);
     return order_key(v != v ? -INFINITY : number(c));
   };
   // 1) exact keys of all experts
@@ -194,7 +200,9 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
       }
     }
   };
-  if (!rough && !direct) exact_keys();
+  // (Direct keys tell neither NaN from -infinity, see `mixed`, nor what ties beside +infinity: a NaN
+  // check in their unrolled code would cost every call 0.4 us)
+  if (!rough && (!direct || m == INFINITY)) exact_keys();
   // 2) groups: L lanes each (of a power of two), the two largest keys of a group in each
   if constexpr (GROUPS) {
     __syncwarp();
@@ -237,6 +245,7 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
     bound = __reduce_max_sync(kFull, v);
     v = v == bound ? 0u : v;
   }
+  const bool mixed = direct && bound <= order_key(-INFINITY);  // -infinity or NaN may be chosen: exact keys tell them apart
   // (K experts have an approximate key of at least it: the exact K-th largest is within the
   // approximation's error of it, and every expert chosen within twice that)
   bound = rough ? topk_impl::candidate_threshold(bound) : max(bound, 1u);
@@ -261,7 +270,7 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
       }
     }
     __syncwarp();
-    if (rough) {  // the candidates' exact keys
+    if (rough || mixed) {  // the candidates' exact keys
       for (int i = lane; i < total; i += 32) {
         const int e = (int)(0xFFFFFFFFu - (uint32_t)ws.list[i]);
         ws.list[i] = rank_key(exact_key(xs[e], __uint_as_float(keys[e])), e);
@@ -283,7 +292,7 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
     place(lane);
     if (total > 32) place(lane + 32);
   } else {
-    if (rough) exact_keys();
+    if (rough || mixed) exact_keys();
     __syncwarp();
 #pragma unroll 1
     for (int k = 0; k < K; ++k) {
@@ -323,14 +332,16 @@ template <bool SOFTMAX, bool TOP2>
 __global__ void __launch_bounds__(32 * kWarps) route_any_kernel(const GroupedArgs a) {
   extern __shared__ float smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  float* key = smem + (size_t)warp * (2 * a.E + MOE_MAX_GROUPS);
-  float* score = key + a.E;
-  float* value = score + a.E;
+  float* score = smem + (size_t)warp * (2 * a.E + MOE_MAX_GROUPS);
+  uint32_t* key = reinterpret_cast<uint32_t*>(score + a.E);  // (0: not to be chosen)
+  uint32_t* value = key + a.E;
   grid_launch_dependents();
   grid_wait();
   const int t = blockIdx.x * warps + warp;
   if (t >= a.T) return;
   const float* x = a.logits + (size_t)t * a.E;
+  const int size = a.E / a.n_group;
+  const bool grouped = a.n_group > 1 && a.topk_group < a.n_group, by_logit = SOFTMAX && !a.bias && !(TOP2 && grouped && size > 1);
   float m = -INFINITY, sum = 0.f;
   if (SOFTMAX) {
     for (int e = lane; e < a.E; e += 32) m = fmaxf(m, x[e]);
@@ -346,37 +357,28 @@ __global__ void __launch_bounds__(32 * kWarps) route_any_kernel(const GroupedArg
     else
       s = xv != xv ? 0.f : spec_sigmoid(xv);
     score[e] = s;
-    key[e] = xv != xv ? -INFINITY : number(a.bias ? __fadd_rn(s, a.bias[e]) : s);
+    key[e] = by_logit ? logit_key(xv, m) : order_key(xv != xv ? -INFINITY : number(a.bias ? __fadd_rn(s, a.bias[e]) : s));
   }
   __syncwarp();
-  if (a.n_group > 1 && a.topk_group < a.n_group) {
-    const int size = a.E / a.n_group;
+  if (grouped) {
     for (int g = 0; g < a.n_group; ++g) {
-      float b1 = -INFINITY, b2 = -INFINITY;  // the lane's two largest keys of the group
-      for (int i = lane; i < size; i += 32) {
-        const float k = key[g * size + i];
-        b2 = fmaxf(b2, fminf(b1, k));
-        b1 = fmaxf(b1, k);
-      }
+      uint32_t b1 = 0, b2 = 0;  // the lane's two largest keys of the group
+      for (int i = lane; i < size; i += 32) merge2(b1, b2, key[g * size + i], 0u);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        const float o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
-        b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
-        b1 = fmaxf(b1, o1);
+        const uint32_t o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+        merge2(b1, b2, o1, o2);
       }
-      if (lane == 0) value[g] = TOP2 && size > 1 ? number(__fadd_rn(b1, b2)) : b1;
+      if (lane == 0)
+        value[g] = TOP2 && size > 1 ? order_key(number(__fadd_rn(topk_impl::key_value(b1), topk_impl::key_value(b2)))) : b1;
     }
     __syncwarp();
     // a group is dropped when at least topk_group groups order before it
     for (int g = 0; g < a.n_group; ++g) {
-      const uint32_t kg = order_key(value[g]);
       int before = 0;
-      for (int o = 0; o < a.n_group; ++o) {
-        const uint32_t ko = order_key(value[o]);
-        before += ko > kg || (ko == kg && o < g);
-      }
+      for (int o = 0; o < a.n_group; ++o) before += value[o] > value[g] || (value[o] == value[g] && o < g);
       if (before >= a.topk_group)
-        for (int i = lane; i < size; i += 32) key[g * size + i] = __uint_as_float(0x7FC00000u);  // (NaN: not kept)
+        for (int i = lane; i < size; i += 32) key[g * size + i] = 0u;
     }
     __syncwarp();
   }
@@ -386,15 +388,14 @@ __global__ void __launch_bounds__(32 * kWarps) route_any_kernel(const GroupedArg
     uint32_t best = 0;
     int at = 0x7FFFFFFF;
     for (int e = lane; e < a.E; e += 32) {
-      const float kv = key[e];
-      const uint32_t o = kv != kv ? 0u : order_key(kv);
+      const uint32_t o = key[e];
       if (o > best) best = o, at = e;
     }
     const uint32_t top = __reduce_max_sync(kFull, best);
     const int win = (int)__reduce_min_sync(kFull, best == top ? (uint32_t)at : 0x7FFFFFFFu);
     if (lane == k) my_id = win, my_s = score[win];
     __syncwarp();
-    if (lane == 0) key[win] = __uint_as_float(0x7FC00000u);
+    if (lane == 0) key[win] = 0u;
     __syncwarp();
   }
   write_weights(a, t, my_id, my_s);
