@@ -528,7 +528,8 @@ int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, co
  * n_pairs is the length of the list (T * topk). Rows of out that no listed pair names
  * are left as they are. A pair code outside [0, n_pairs), or an input row outside
  * [0, a_rows), is skipped and sets MOE_DEVERR_ROW_INDEX; offsets outside [0, n_pairs]
- * count as the nearest bound.
+ * count as the nearest bound, and an offset below the one before it ends an empty list.
+ * What no list holds is not read: offsets may start past 0 (the lists of some experts).
  * Requirements: n_pairs >= 0, N >= 0 (either 0 launches nothing), 1 <= E <=
  * MOE_MAX_EXPERTS, topk >= 1, a_rows >= 1; K, alignment and numerics as fp8_block_gemm.
  * ------------------------------------------------------------------------------- */
