@@ -160,9 +160,12 @@ __global__ void __launch_bounds__(Narrow<BN, ROWS, NG, CG>::kThreads, Narrow<BN,
         ++issued;
       }
     }
-    // the copies still in flight land before the CTA may exit
-    for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-      mbar_wait(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
+    // The CTA may not exit with arrivals on its barriers to come: the issuer's last commits, which are
+    // after the copies; without them (it gave up) the copies in flight.
+    const int first = issued > stages ? issued - stages : 0;
+    for (int i = first; i < issued && ok; ++i)
+      ok = __all_sync(kFullMask, mbar_wait_asleep(empty(i % stages), (uint32_t)(i / stages) & 1u, g.err));
+    for (int i = first; i < issued && !ok; ++i) mbar_wait_asleep(full(i % stages), (uint32_t)(i / stages) & 1u, g.err);
   } else if (warp == C::kEpiWarps + 1) {  // MMA issuer
     // (the whole warp walks the loop, so that descriptors stay in uniform registers)
     constexpr uint32_t idesc = instr_desc_e4m3(BN, 128);

@@ -247,10 +247,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           ++issued;
         }
       }
-      // the pair's copies still in flight land before either CTA may exit
-      if (half == 0)
-        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-          mbar_wait_asleep(full(i % kStages), (uint32_t)(i / kStages) & 1u, g.err);
+      // Neither CTA may exit with arrivals on its barriers to come: the issuers' last commits, which
+      // are after the copies; without them (an issuer gave up) the pair's copies in flight.
+      const int first = issued > kStages ? issued - kStages : 0;
+      for (int i = first; i < issued && ok; ++i)
+        ok = __all_sync(kFullMask, mbar_wait_asleep(empty(i % kStages), (uint32_t)(i / kStages) & 1u, g.err));
+      if (half == 0 && !ok)
+        for (int i = first; i < issued; ++i) mbar_wait_asleep(full(i % kStages), (uint32_t)(i / kStages) & 1u, g.err);
     } else if (warp == kEpiWarps + 1 || warp == kEpiWarps + 2) {  // MMA issuers
       // (the whole warp walks the loop, so that descriptors stay in uniform registers)
       if (half == 0) {
