@@ -172,7 +172,7 @@ extern "C" int moe_expert_gemm(const uint8_t* a, const float* a_scales, int64_t 
   g.a = a, g.sa = a_scales, g.w = w, g.sw = w_scales, g.out = out, g.f32 = out_dtype == MOE_DTYPE_F32;
   g.M = n_pairs, g.N = N, g.K = K, g.E = E;
   g.offsets = offsets, g.pairs = pairs, g.a_rows = a_rows, g.topk = topk, g.in_rows = in_rows, g.out_rows = out_rows;
-  if (E < 1 || topk < 1 || a_rows < 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (E < 1 || topk < 1 || a_rows < 0 || (a_rows == 0 && n_pairs != 0)) return MOE_ERR_INVALID_ARGUMENT;
   if (in_rows != MOE_ROWS_TOKEN && in_rows != MOE_ROWS_LIST && in_rows != MOE_ROWS_PAIR) return MOE_ERR_INVALID_ARGUMENT;
   if (out_rows != MOE_ROWS_LIST && out_rows != MOE_ROWS_PAIR) return MOE_ERR_INVALID_ARGUMENT;
   const int st = check(g, out_dtype);

@@ -43,3 +43,12 @@ def test_descending_offsets(moe, offsets, in_rows):
             src = p // topk if in_rows == "ROWS_TOKEN" else p
             gemm_check(out[torch.from_numpy(p.astype(np.int64)).cuda()], a[src], sa[src], w[e], sw[e])
     assert (out[torch.from_numpy(pairs[owner == -1].astype(np.int64)).cuda()] == 3.0).all()
+
+
+def test_empty_batch(moe):
+    """No tokens: an output of no rows, by every row mode."""
+    f = lambda *s: torch.zeros(*s, device="cuda")
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    for rows in (moe.ROWS_TOKEN, moe.ROWS_LIST, moe.ROWS_PAIR):
+        assert moe.expert_gemm(u8(0, 32), f(0, 1), u8(4, 8, 32), f(4, 1, 1), i32(5), i32(0), 2, in_rows=rows).shape == (0, 8)
