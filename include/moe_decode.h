@@ -531,8 +531,9 @@ int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, co
  * count as the nearest bound, and an offset below the one before it ends an empty list.
  * What no list holds is not read: offsets may start past 0 (the lists of some experts).
  * Requirements: n_pairs >= 0, N >= 0 (either 0 launches nothing), 1 <= E <=
- * MOE_MAX_EXPERTS, topk >= 1, a_rows >= 1 (>= 0 with n_pairs = 0); K, alignment and
- * numerics as fp8_block_gemm.
+ * MOE_MAX_EXPERTS, topk >= 1, a_rows >= 1 (>= 0 with n_pairs = 0); n_pairs < 2^31 - 2^16
+ * and a_rows < 2^31 (MOE_ERR_CAPACITY); K, the other capacities, alignment and numerics as
+ * fp8_block_gemm.
  * ------------------------------------------------------------------------------- */
 #define MOE_ROWS_TOKEN 0
 #define MOE_ROWS_LIST 1

@@ -74,6 +74,7 @@ size_t list_copy_bytes(int n_pairs, int K) {
 }
 
 constexpr int kCopyThreads = 256;
+constexpr int kMaxPairs = 0x7FFFFFFF - (1 << 16);  // (loops and tiles step past the end)
 
 // Whether a list holds position i (by a warp); -1: neither it nor any later one.
 __device__ __forceinline__ int listed(const int32_t* offsets, int E, int i) {
@@ -178,7 +179,7 @@ extern "C" int moe_expert_gemm(const uint8_t* a, const float* a_scales, int64_t 
   const int st = check(g, out_dtype);
   if (st != MOE_OK || n_pairs == 0 || N == 0) return st;
   if (!offsets || !pairs) return MOE_ERR_INVALID_ARGUMENT;
-  if (E > MOE_MAX_EXPERTS) return MOE_ERR_CAPACITY;
+  if (E > MOE_MAX_EXPERTS || n_pairs > kMaxPairs) return MOE_ERR_CAPACITY;
   if (!aligned(offsets, 4) || !aligned(pairs, 4) || !aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
   const size_t need = moe_expert_gemm_workspace(n_pairs, E, N, K, in_rows);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;

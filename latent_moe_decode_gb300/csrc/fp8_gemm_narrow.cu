@@ -62,7 +62,7 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, const int* table, int
     r.pos = lo + local % c * BN;
     r.cnt = min(BN, hi - r.pos);
   } else {
-    const int mt = (g.M + BN - 1) / BN;
+    const int mt = (g.M - 1) / BN + 1;
     r.e = 0;
     r.n0 = t / mt * 128;
     r.pos = t % mt * BN;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(Narrow<BN, ROWS, NG, CG>::kThreads, Narrow<BN,
     tile_table(g, BN, table, warp_sums);
     tiles = min(table[g.E], max_row_tiles) * g.nbn;
   } else {
-    tiles = g.nbn * ((g.M + BN - 1) / BN);
+    tiles = g.nbn * ((g.M - 1) / BN + 1);
   }
   const int rank = blockIdx.x % S, t0 = blockIdx.x / S, step = gridDim.x / S;
   const int kb0 = (int)((long long)rank * g.nbk / S), kb1 = (int)((long long)(rank + 1) * g.nbk / S);

@@ -414,7 +414,7 @@ size_t one_wave_pad(long long blocks, size_t fixed, const DeviceInfo& dev) {
 
 template <int NJ, bool VEC, bool GROUPS>
 int launch_registers(const GroupedArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  const unsigned blocks = (unsigned)((a.T + kWarps - 1) / kWarps);
+  const unsigned blocks = (unsigned)((a.T - 1) / kWarps + 1);
   const size_t fixed = kWarps * (sizeof(RouteScratch) + 2 * NJ * 32 * sizeof(uint32_t));
   return launch_pdl(route_kernel<NJ, VEC, GROUPS>, dim3(blocks), dim3(32 * kWarps), one_wave_pad(blocks, fixed, dev), s, a);
 }
@@ -463,5 +463,5 @@ extern "C" int moe_topk_route_grouped(const float* logits, const float* bias, in
   const size_t smem = (size_t)warps * (2 * E + MOE_MAX_GROUPS) * sizeof(float);  // at most 34 KB
   auto kern = a.softmax ? (a.top2 ? route_any_kernel<true, true> : route_any_kernel<true, false>)
                         : (a.top2 ? route_any_kernel<false, true> : route_any_kernel<false, false>);
-  return launch_pdl(kern, dim3((T + warps - 1) / warps), dim3(32 * warps), smem, as_cuda(stream), a);
+  return launch_pdl(kern, dim3((T - 1) / warps + 1), dim3(32 * warps), smem, as_cuda(stream), a);
 }

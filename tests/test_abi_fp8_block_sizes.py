@@ -22,3 +22,9 @@ def expert_gemm(lib, rows, n, ws=None, wb=0, E=4, N=8, K=32):
 def test_expert_gemm_of_an_empty_batch(lib):
     assert expert_gemm(lib, 0, 0) == 0
     assert expert_gemm(lib, 0, 1) == 1 and expert_gemm(lib, -1, 0) == 1 and expert_gemm(lib, -1, 8) == 1
+
+
+def test_expert_gemm_of_more_pairs_than_its_indices_hold(lib):
+    """The list copy's loop steps past the last pair by what its warps take at a time."""
+    for n in (2 ** 31 - 1, 2 ** 31 - 2 ** 16):
+        assert expert_gemm(lib, 1, n, A16, 2 ** 62) == 3
