@@ -531,7 +531,9 @@ int launch_bn(int bn, const GemmArgs& g, long long a_rows, int sm_count, cudaStr
   switch (bn) {
     case 16: return plan<16, ROWS>(g, a_rows, sm_count, stream);
     case 32: return plan<32, ROWS>(g, a_rows, sm_count, stream);
-    case 64: return plan<64, ROWS>(g, a_rows, sm_count, stream);
+    case 64:
+      if constexpr (ROWS != kNamed) return plan<64, ROWS>(g, a_rows, sm_count, stream);  // (lists this long are copied)
+      return MOE_ERR_INVALID_ARGUMENT;
     default:
       if constexpr (ROWS == kDense) return plan<128, kDense>(g, a_rows, sm_count, stream);
       return MOE_ERR_INVALID_ARGUMENT;
