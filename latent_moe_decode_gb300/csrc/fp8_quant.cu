@@ -12,8 +12,11 @@
 //   - the four maxima of a half-warp are reduced together, five exchanges instead of
 //     sixteen, which leaves each on four lanes;
 //   - those lanes divide for that block alone, and hand the multiplier back;
-//   - silu is 2^x and 1/x of the special-function unit. Its error is below 2^-20 of the
-//     value to |gate| = 12, where silu is 7e-5 of gate.
+//   - silu is 2^x and 1/x of the special-function unit. Over all BF16 gates its error is at
+//     most 0.83 x 2^-20 of the value to |gate| = 12 (rounding the exponent's argument alone can
+//     make 0.7) and 3.4 x 2^-20 to 64, measured with the scale's division (tests; the bound
+//     that follows from the operations is 1.45 x 2^-20 to 12). A code moves only beside a tie:
+//     39 of 16.7 million, as of the plain form in FP32.
 #include "fp8_block.cuh"
 
 namespace moe {
