@@ -472,7 +472,8 @@ int moe_topk_route_grouped(const float* logits, const float* bias, int T, int E,
  *   q     = E4M3( v * (448 / amax) ), or E4M3( v / scale ) for the power of two: rounded
  *           to nearest even, saturated at +-448
  * v is the row itself, or (fp8_block_quantize_swiglu) silu(gate) * up of a row of
- * 2 * cols values [gate | up], silu(g) = g / (1 + exp(-g)), computed and kept in FP32.
+ * 2 * cols values [gate | up], silu(g) = g / (1 + exp(-g)), computed and kept in FP32
+ * (within 1.45 x 2^-20 of its value to |g| = 12, 4.4 x 2^-20 to 64).
  * A block of zeros has scale 1; amax below 2^-110 counts as 2^-110 in the scale; a block
  * with a NaN or an infinity has the scale NaN and every code 0x7F.
  *
@@ -480,8 +481,8 @@ int moe_topk_route_grouped(const float* logits, const float* bias, int T, int E,
  *   q       device, E4M3 [rows, cols]          output
  *   scales  device, FP32 [rows, nb(cols)]      output
  * Requirements: rows >= 0 (0 launches nothing), cols >= 8, cols % 8 == 0, ldx at least
- * the row's length and ldx % 8 == 0 (MOE_ERR_INVALID_ARGUMENT); rows * nb(cols) < 2^31
- * (MOE_ERR_CAPACITY); x 16-byte, q 8-byte, scales 4-byte aligned.
+ * the row's length and ldx % 8 == 0, cols <= 2^29 (MOE_ERR_INVALID_ARGUMENT); rows *
+ * nb(cols) < 2^31 - 2^24 (MOE_ERR_CAPACITY); x 16-byte, q 8-byte, scales 4-byte aligned.
  * ------------------------------------------------------------------------------- */
 #define FP8_SCALE_AMAX 0
 #define FP8_SCALE_POW2 1
@@ -501,8 +502,9 @@ int fp8_block_quantize_swiglu(const uint16_t* x, int64_t ldx, int rows, int cols
  *   w, w_scales  device, E4M3 [N, K], FP32 [nb(N), nb(K)]
  *   out          device, [M, N] of out_dtype (MOE_DTYPE_F32 or MOE_DTYPE_BF16)
  * Requirements: M >= 0, N >= 0 (either 0 launches nothing), K >= 16, K % 16 == 0
- * (MOE_ERR_INVALID_ARGUMENT); a, w 16-byte aligned, scales 4-byte, out to its element.
- * Deterministic.
+ * (MOE_ERR_INVALID_ARGUMENT); N < 2^31 - 128 (of all experts together: E * N), and tiles
+ * of the output, of 16 x 128 values at least, fewer than 2^31 - 2^16 (MOE_ERR_CAPACITY); a,
+ * w 16-byte aligned, scales 4-byte, out to its element. Deterministic.
  * ------------------------------------------------------------------------------- */
 int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales, void* out,
                    int out_dtype, int M, int N, int K, moe_stream_t stream);
@@ -530,6 +532,8 @@ int fp8_block_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, co
  * [0, a_rows), is skipped and sets MOE_DEVERR_ROW_INDEX; offsets outside [0, n_pairs]
  * count as the nearest bound, and an offset below the one before it ends an empty list.
  * What no list holds is not read: offsets may start past 0 (the lists of some experts).
+ * Lists that overlap (offsets that descend) are worked through to n_pairs positions in all;
+ * what lies beyond may be left out, and a row that several hold gets one of their products.
  * Requirements: n_pairs >= 0, N >= 0 (either 0 launches nothing), 1 <= E <=
  * MOE_MAX_EXPERTS, topk >= 1, a_rows >= 1 (>= 0 with n_pairs = 0); n_pairs < 2^31 - 2^16
  * and a_rows < 2^31 (MOE_ERR_CAPACITY); K, the other capacities, alignment and numerics as

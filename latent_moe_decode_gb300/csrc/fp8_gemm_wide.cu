@@ -18,7 +18,7 @@
 //     both), so that the row-major scales are fetched once per CTA and not per warp.
 // A persistent grid of pairs walks the tiles, row tiles of the same weights side by side.
 // Grouped, the rows of an expert's list are read as one box, so they have to lie in list
-// order: launch_wide copies rows that do not (MOE_ROWS_TOKEN, MOE_ROWS_PAIR) there first.
+// order: the caller copies rows that do not (MOE_ROWS_TOKEN, MOE_ROWS_PAIR) there first.
 // (TMA's gather4, which could fetch them from where they are, moved 128 rows x 128 bytes
 // in 2300 cycles, against 900 for a whole block with the copies: 4096 tokens x 8 of 64
 // experts took 1166 us with it.)

@@ -168,7 +168,7 @@ __device__ __forceinline__ void route_token(const GroupedArgs& a, int t, RouteSc
           if (!by_logit) xs[e] = v != v ? v : x;
         }
       sum = warp_sum(sum);
-      inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+      inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;  // (two roundings a score, not a division)
     }
   }
   auto score = [&](float v) {  // of what xs holds
