@@ -76,3 +76,26 @@ def test_results_stay_while_the_current_stream_reads_them(moe):
         moe.fp8_block_quantize_rows(zeros, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(copy, expect)
+
+
+def test_another_stream_in_a_captured_fork(moe):
+    """A call on a side stream of a capture, its results and scratch allocated there, replayed over changed rows."""
+    o = operands()
+    offsets, pairs = moe.build_routing_lists(o["ids"], o["E"])
+    args = (o["a"], o["sa"], o["w"], o["sw"], offsets, pairs, o["topk"])
+    moe.expert_gemm(*args)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        out = moe.expert_gemm(*args, stream=side)
+        codes = moe.fp8_block_quantize_rows(o["x"])  # (beside it)
+        main.wait_stream(side)
+    for _ in range(3):
+        o["a"].copy_(o["a"].roll(1, 0))
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, moe.expert_gemm(*args))
+    assert torch.equal(codes[0], moe.fp8_block_quantize_rows(o["x"])[0])
+    assert moe.device_error() == 0
