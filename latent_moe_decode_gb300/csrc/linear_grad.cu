@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs g) {
     }
   }
   if (!g.dbias) return;
+  __syncwarp();  // (the lanes of a warp end their rows apart)
 #pragma unroll
   for (int i = 0; i < 8; ++i) part[r][VEC ? 8 * lane + i : lane + 8 * i] = sum[i];
   __syncthreads();
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs g) {
     for (int i = 0; i < kRowLanes; ++i) s += part[i][threadIdx.x];
     strip[threadIdx.x] = s;
   }
+  __syncwarp();
   cluster_sync();  // (the cluster is the strip's CTAs, ranks in the order of blockIdx.y)
   if (blockIdx.y == 0 && threadIdx.x < kStrip) {
     float s = 0.f;
@@ -126,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs g) {
     const int n = blockIdx.x * kStrip + threadIdx.x;
     if (n < g.N) g.dbias[n] = s;
   }
+  __syncwarp();
   cluster_sync();  // no CTA leaves while its sums may be read
 }
 

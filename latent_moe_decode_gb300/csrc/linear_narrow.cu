@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int h = 0; h < W; h += 16) fetch_residual(g, m0 + c + h, n, cnt - c - h, res[h / 16]);
       }
+      __syncwarp();  // (lanes beyond N had nothing to fetch; what follows is one instruction of the whole warp)
       for (int r = 0; r < runs; ++r) {
         uint32_t v[W];
         if constexpr (W == 16)
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int j = 0; j < 16; ++j) zh[j] = z[h + j];
           if (n < g.N && c + h < cnt) finish_rows<GATED>(g, m0 + c + h, n, cnt - c - h, zh, zh, res[h / 16]);
         }
+        __syncwarp();
         return;
       }
       if (!free) cluster_wait(), free = true;
@@ -289,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     tcgen05_before_sync();
   }
+  __syncwarp();
   if (!free) cluster_wait();
   __syncwarp();
   if (adds) {
@@ -302,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float r[16] = {};
     place(threadIdx.x, &c, &n);
     if (!GATED && (int)threadIdx.x < items && n < g.N) fetch_residual(g, m0 + c, n, min(cnt, 4 * (first + have)) - c, r);
+    __syncwarp();
     if (S > 1)
       mbar_wait_asleep(came, 0u, err);
     else
