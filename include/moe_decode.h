@@ -615,7 +615,9 @@ int moe_block_norm(const uint16_t* y, int64_t ldy, const void* residual, int res
  * K < 2^31 - 2^16 (MOE_ERR_CAPACITY); x, w 16-byte aligned, the rest to their elements.
  * Rows that start at multiples of 16 or 32 bytes are stored in wide pieces. Sums of an FP32
  * result are taken in runs of 512 of K (to 768 for few rows, 1024 for the first two of long sums of
- * many), each rounded to nearest as it is added: within 1e-6 of the whole, rms, at K to 7168. An activation of an FP32
+ * many), each rounded to nearest as it is added: within 1e-6 of the whole, rms, at K to 7168. Those of a
+ * BF16 result run over up to 8192 of K (what the tensor core cuts off towards zero: 1e-5 of the whole, rms, 5e-5 where all
+ * terms have one sign), longer ones in runs. An activation of an FP32
  * result is evaluated to within 1e-6 of its value (0 where a sigmoid is below 2^-126; gelu's tanh form to
  * 3.6e-7 more for each unit of its argument), of a BF16 result to some 2^-18. A NaN stays one; -infinity times a sigmoid or distribution of 0 is NaN. Deterministic.
  * ------------------------------------------------------------------------------- */
@@ -625,7 +627,7 @@ int bf16_linear(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, 
 
 /* Its gradients, from that of out (which is the residual's as well):
  *   dz    = dout act'(pre)      (BF16_ACT_NONE: dout, and pre is not read)
- *   dx    = dz w,  dw = dz^T x  FP32 sums, rounded once to dx_dtype / dw_dtype
+ *   dx    = dz w,  dw = dz^T x  FP32 sums as bf16_linear's, rounded once to dx_dtype / dw_dtype
  *   dbias = sum_t dz[t]         FP32
  * dz goes to the products rounded once to BF16, the type they multiply (dout is BF16 already:
  * without an activation nothing is rounded), to dbias in FP32; act' within some 2^-18. Where

@@ -391,7 +391,7 @@ NarrowPlan plan_narrow(const Product& s, bool gated, const DeviceInfo& dev) {
       const long long ctas = tiles * splits;
       for (int per_sm = 1; per_sm <= 2; ++per_sm) {
         if (per_sm == 2 && ctas <= dev.sm_count) continue;
-        if (s.e.out_f32 && (nbk - 1) / splits + 1 > kMaxExactRun * (512 / per_sm / bn)) continue;
+        if ((nbk - 1) / splits + 1 > (s.e.out_f32 ? kMaxExactRun : kMaxCutBlocks) * (512 / per_sm / bn)) continue;
         if (bn > 512 / per_sm || partial_bytes(bn, splits) > room(per_sm)) continue;
         if (splits > 1 && tiles > (long long)per_sm * max_clusters(splits)) continue;
         if (ctas > (long long)dev.sm_count * per_sm) continue;  // (more than one wave is the wide kernel's)

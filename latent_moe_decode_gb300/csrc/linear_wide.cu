@@ -11,9 +11,11 @@
 // Two accumulators in TMEM: a tile's epilogue runs under the next tile's multiplication.
 // A persistent grid of pairs walks the tiles of one or two products.
 // FP32 results: the tensor core cuts its running sum off after every 16 values of K, always
-// towards zero, which adds up to some 2e-8 of the sum a step (9e-6 at K = 7184). There a tile's
-// sums are taken in runs of kRun blocks, the runs added in registers with rounding to nearest
-// (4e-7). The registers are read from TMEM under the next run's multiplication.
+// towards zero, which adds up to some 2e-8 of the sum a step (9e-6 at K = 7184), to 1e-7 where all terms
+// have one sign. There a tile's sums are taken in runs of kRun blocks, the runs added in registers with
+// rounding to nearest (4e-7). The registers are read from TMEM under the next run's multiplication.
+// So are the sums of BF16 results over more than kWhole blocks (weights' gradients over many rows: one
+// run of 2^20 terms of one sign was 6.6e-3 too small, more than the rounding to BF16).
 #include "linear.cuh"
 
 namespace moe {
@@ -27,6 +29,7 @@ constexpr int kMaxCols = 256;
 constexpr int kHalf = 128 * kBlockK * 2;   // bytes of one CTA's rows of a, or of b, of a stage
 constexpr int kMaxStages = 10;
 constexpr int kRun = 8;                    // blocks of K that an FP32 result's sums take in one go
+constexpr int kWhole = kMaxCutBlocks;       // that a BF16 result's sums take whole
 constexpr int kPadBytes = 32 * 32 * 4;      // of an epilogue warp
 
 struct Part {  // of the launch: one product
@@ -287,8 +290,10 @@ __device__ __forceinline__ void finish_gated(const Part& p, const Chunk& k, floa
   store_rows(e.out, e.ldo, k, 0, g, pad);
 }
 
-// What a kernel computes: BF16 products, products some of which are FP32, gated pairs.
-enum Kind { kBf16, kF32, kGated };
+// What a kernel computes: BF16 products, products whose sums are taken in runs (FP32 results among them),
+// gated pairs, gated pairs in runs.
+enum Kind { kBf16, kF32, kGated, kGatedRuns };
+constexpr bool is_gated(Kind kind) { return kind == kGated || kind == kGatedRuns; }
 
 struct Tile {
   int m0, n0;  // this CTA's first row of a, the tile's first column of out
@@ -296,7 +301,7 @@ struct Tile {
 
 template <Kind KIND>
 __device__ __forceinline__ Tile tile_at(const Part& p, int t, int half) {
-  return {t % p.row_tiles * kRows + half * 128, t / p.row_tiles * (KIND == kGated ? p.bn / 2 : p.bn)};
+  return {t % p.row_tiles * kRows + half * 128, t / p.row_tiles * (is_gated(KIND) ? p.bn / 2 : p.bn)};
 }
 
 // The block after the run that starts with k0.
@@ -305,7 +310,7 @@ __device__ __forceinline__ int run_end(const Part& p, int k0) { return min(k0 + 
 template <Kind KIND>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     linear_wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Parts g, uint32_t* err) {
-  constexpr bool GATED = KIND == kGated;
+  constexpr bool GATED = is_gated(KIND);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4];
   __shared__ uint32_t tmem_slot;
@@ -508,6 +513,39 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int l = 0; l < 16 * (kPieces - 1); ++l) acc[l] = acc[l + 16];
         }
+      } else if constexpr (KIND == kGatedRuns) {
+        // Pieces of 16 columns of both halves, every second one: the j-th starts at piece(j).
+        constexpr int kPieces = kMaxCols / 64;
+        auto piece = [&](int j) { return 32 * j + 16 * cg; };
+        float acc[32 * kPieces];
+#pragma unroll
+        for (int j = 0; j < 32 * kPieces; ++j) acc[j] = 0.f;
+        for (int k0 = 0; k0 < p.nbk; k0 = run_end(p, k0)) {
+          if (!filled()) break;
+#pragma unroll
+          for (int j = 0; j < 2 * kPieces; ++j) {
+            if (piece(j / 2) >= cols) break;
+            uint32_t v[16];
+            tmem_ld16(tl + (i & 1u) * kMaxCols + (j & 1 ? p.bn / 2 : 0) + piece(j / 2), v);
+            tmem_wait_ld();
+            tmem_loaded(v);
+#pragma unroll
+            for (int l = 0; l < 16; ++l) acc[16 * j + l] = __fadd_rn(acc[16 * j + l], __uint_as_float(v[l]));
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll 1
+        for (int j = 0; j < kPieces; ++j) {
+          if (piece(j) >= cols) break;
+          float a[16], b[16];
+#pragma unroll
+          for (int l = 0; l < 16; ++l) a[l] = acc[l], b[l] = acc[16 + l];
+          finish_gated(p, chunk(piece(j), 16), a, b, box.pad);
+          __syncwarp();
+#pragma unroll
+          for (int l = 0; l < 32 * (kPieces - 1); ++l) acc[l] = acc[l + 32];
+        }
       } else {
         if (!filled()) break;
         const uint32_t ta = tl + (i & 1u) * kMaxCols;
@@ -578,7 +616,7 @@ bool make_out_map(CUtensorMap* m, const void* p, long long ld, int rows, int col
 
 template <Kind KIND>
 int launch(const Product* products, int count, const WidePlan& plan, cudaStream_t stream, uint32_t* err) {
-  constexpr bool GATED = KIND == kGated;
+  constexpr bool GATED = is_gated(KIND);
   Parts parts = {};
   Maps maps = {};
   int pairs = 0;
@@ -586,7 +624,8 @@ int launch(const Product* products, int count, const WidePlan& plan, cudaStream_
     const Product& s = products[i];
     Part& p = parts.p[i];
     p.e = s.e, p.M = s.M, p.N = s.N, p.nbk = (s.K - 1) / kBlockK + 1;
-    p.run = s.e.out_f32 ? kRun : p.nbk, p.run0 = s.e.out_f32 && p.nbk >= 7 * kRun ? 2 * kRun : p.run;
+    p.run = s.e.out_f32 ? kRun : p.nbk > kWhole ? 2 * kRun : p.nbk;
+    p.run0 = s.e.out_f32 && p.nbk >= 7 * kRun ? 2 * kRun : p.run;
     p.a_transposed = s.a.transposed, p.b_transposed = s.b.transposed;
     p.bn = plan.bn[i], p.pairs = plan.pairs[i];
     pairs += p.pairs;
@@ -684,9 +723,10 @@ WidePlan plan_wide(const Product* products, int count, bool gated, const DeviceI
 int launch_wide(const Product* products, int count, bool gated, const WidePlan& plan, const DeviceInfo& dev, cudaStream_t stream) {
   for (int i = 0; i < count; ++i)
     if (tile_count(products[i], gated, plan.bn[i]) >= (1LL << 31) - (1 << 16)) return MOE_ERR_CAPACITY;
-  if (gated) return launch<kGated>(products, count, plan, stream, dev.error_word);
-  return products[0].e.out_f32 || (count > 1 && products[1].e.out_f32) ? launch<kF32>(products, count, plan, stream, dev.error_word)
-                                                                       : launch<kBf16>(products, count, plan, stream, dev.error_word);
+  bool runs = false;
+  for (int i = 0; i < count; ++i) runs = runs || products[i].e.out_f32 || products[i].K > kWhole * kBlockK;
+  if (gated) return runs ? launch<kGatedRuns>(products, count, plan, stream, dev.error_word) : launch<kGated>(products, count, plan, stream, dev.error_word);
+  return runs ? launch<kF32>(products, count, plan, stream, dev.error_word) : launch<kBf16>(products, count, plan, stream, dev.error_word);
 }
 
 }  // namespace linear_impl
