@@ -632,6 +632,7 @@ int bf16_linear(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, 
  * dz goes to the products rounded once to BF16, the type they multiply (dout is BF16 already:
  * without an activation nothing is rounded), to dbias in FP32; act' within some 2^-18. Where
  * a sigmoid has reached 0 or 1 its slope counts as 0, so that act'(+-infinity) is the limit.
+ * relu' is 1 where z > 0 and else 0 (a NaN's too); the others' at NaN is NaN.
  *   dout       device, BF16 [T, N], rows ldd apart; pre BF16 [T, N], rows ldp apart
  *   dx         device, [T, K] of dx_dtype, rows lddx apart    output, or NULL
  *   dw         device, [N, K] of dw_dtype, rows lddw apart    output, or NULL

@@ -185,7 +185,7 @@ __device__ __forceinline__ void with_slope(int act, const float (&z)[2], float (
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         value[i] = act == BF16_ACT_RELU ? relu(z[i]) : z[i];
-        slope[i] = act == BF16_ACT_RELU && z[i] <= 0.f ? 0.f : 1.f;
+        slope[i] = act == BF16_ACT_NONE || z[i] > 0.f ? 1.f : 0.f;  // (relu of a NaN: 0)
       }
       break;
   }
