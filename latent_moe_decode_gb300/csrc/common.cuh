@@ -12,6 +12,7 @@ namespace moe {
 // Host side: per-device facts, the device error word, PDL launches.
 
 struct DeviceInfo {
+  int device = 0;             // its number
   int sm_count = 0;
   int cc_major = 0, cc_minor = 0;
   int smem_per_sm = 0;        // shared memory an SM holds (bytes)

@@ -448,32 +448,17 @@ struct Split {
   static_assert((size_t)kMost * C::kStageBytes >= (size_t)BN * 512, "the stages hold a partial tile");
 };
 
-// Clusters of s such CTAs that are resident at once (clusters stay within a GPC, so whole-SM
-// CTAs leave some of its SMs over); looked up once.
+// Clusters of s such CTAs that are resident at once, looked up once a device (none where that fails).
 template <int BN>
 int max_clusters(int s) {
-  static std::atomic<int> known[kMaxSplits + 1];
-  int n = known[s].load(std::memory_order_relaxed);
-  if (n != 0) return n;
+  static PerDevice<kMaxSplits + 1> known;
   using P = Split<BN>;
-  auto kern = narrow_kernel<BN, kDense, 1, P::kParts>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(s * 64);
-  cfg.blockDim = dim3(P::C::kThreads);
-  cfg.dynamicSmemBytes = P::kShare - kStaticSmem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = s, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - kStaticSmem) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
-  }
-  if (n <= 0) n = -1;
-  known[s].store(n, std::memory_order_relaxed);
-  return n;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  return known.get(dev, s, [&] {
+    return resident_clusters(reinterpret_cast<const void*>(narrow_kernel<BN, kDense, 1, P::kParts>), s, P::C::kThreads, P::kShare - kStaticSmem,
+                             kMaxSmem - kStaticSmem);
+  });
 }
 
 // The CTAs of a tile: the most whose clusters are all resident at once where a CTA takes an

@@ -42,7 +42,7 @@ int check_sizes(int T, int N, int K, bool gated) {
 // The plans of the sizes that a thread asked for last: the search takes 1 to 4 us of the host, half of what is
 // left of a call.
 struct Choice {
-  int M, N, K, kind, sms;  // kind: what else a plan depends on (0: an empty entry)
+  int M, N, K, kind, device;  // kind: what else a plan depends on (0: an empty entry)
   bool narrow;
   NarrowPlan n;
   WidePlan both, one;  // (forward: one)
@@ -52,26 +52,30 @@ int kind_of(const Product& p) {
   return (e.out_f32 ? 1 : 0) | (e.residual ? (e.residual_f32 ? 4 : 2) : 0) | (e.pre ? 8 : 0);
 }
 template <typename Make>
-const Choice& choose(int M, int N, int K, int kind, int sms, Make make) {
+int choose(int M, int N, int K, int kind, int device, const Choice** choice, Make make) {
   static thread_local Choice known[64];
   const uint32_t h = ((uint32_t)M * 2654435761u) ^ ((uint32_t)N * 2246822519u) ^ ((uint32_t)K * 3266489917u) ^ ((uint32_t)kind * 668265263u);
   Choice& c = known[(h ^ h >> 15) & 63];
-  if (c.M != M || c.N != N || c.K != K || c.kind != kind || c.sms != sms) {
-    make(&c);
-    c.M = M, c.N = N, c.K = K, c.kind = kind, c.sms = sms;
+  if (c.M != M || c.N != N || c.K != K || c.kind != kind || c.device != device) {
+    c.kind = 0;
+    MOE_TRY(make(&c));
+    c.M = M, c.N = N, c.K = K, c.kind = kind, c.device = device;
   }
-  return c;
+  *choice = &c;
+  return MOE_OK;
 }
 
 int forward(const Product& p, bool gated, cudaStream_t stream) {
   DeviceInfo dev;
   MOE_TRY(current_device(&dev));
-  const Choice& c = choose(p.M, p.N, p.K, 64 | (gated ? 128 : 0) | kind_of(p), dev.sm_count, [&](Choice* c) {
-    c->n = plan_narrow(p, gated, dev);
+  const Choice* c;
+  MOE_TRY(choose(p.M, p.N, p.K, 64 | (gated ? 128 : 0) | kind_of(p), dev.device, &c, [&](Choice* c) {
+    MOE_TRY(plan_narrow(p, gated, dev, &c->n));
     c->one = plan_wide(&p, 1, gated, dev);
     c->narrow = c->n.ns < c->one.ns;
-  });
-  return c.narrow ? launch_narrow(p, gated, c.n, dev, stream) : launch_wide(&p, 1, gated, c.one, dev, stream);
+    return MOE_OK;
+  }));
+  return c->narrow ? launch_narrow(p, gated, c->n, dev, stream) : launch_wide(&p, 1, gated, c->one, dev, stream);
 }
 
 // Rows of dz start at multiples of 128 bytes, so that a box's rows are whole lines (129 x 2072 x 2064 10.2 us, 12.4 with
@@ -117,11 +121,14 @@ int backward_products(const uint16_t* dz, long long ldz, const uint16_t* x, int6
   pw.e.out = g.dw, pw.e.ldo = g.ldw, pw.e.out_f32 = g.dw && g.dw_dtype == MOE_DTYPE_F32;
   // Both in one launch, or dx by the narrow kernel and dw after it (a launch more, of which the first one's end hides
   // some). Whether dw is asked for does not enter: dx alone is what it is beside a dw in BF16.
-  const Choice& c = choose(T, n, K, 256 | kind_of(px) | kind_of(pw) << 4, dev.sm_count, [&](Choice* c) {
+  const Choice* found;
+  MOE_TRY(choose(T, n, K, 256 | kind_of(px) | kind_of(pw) << 4, dev.device, &found, [&](Choice* c) {
     c->both = plan_wide(p, 2, false, dev), c->one = plan_wide(&pw, 1, false, dev);
-    c->n = plan_narrow(px, false, dev);
+    MOE_TRY(plan_narrow(px, false, dev, &c->n));
     c->narrow = c->n.ns + c->one.ns - 1000 < c->both.ns;
-  });
+    return MOE_OK;
+  }));
+  const Choice& c = *found;
   if (g.dx && g.dw && !c.narrow) return launch_wide(p, 2, false, c.both, dev, stream);
   if (g.dx) MOE_TRY(c.narrow ? launch_narrow(px, false, c.n, dev, stream) : launch_wide(&px, 1, false, plan_wide(&px, 1, false, dev), dev, stream));
   return g.dw ? launch_wide(&pw, 1, false, c.one, dev, stream) : MOE_OK;

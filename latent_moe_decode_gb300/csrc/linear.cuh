@@ -58,7 +58,7 @@ struct NarrowPlan {
   int bn, splits, per_sm;
   double ns;
 };
-NarrowPlan plan_narrow(const Product& product, bool gated, const DeviceInfo& dev);
+int plan_narrow(const Product& product, bool gated, const DeviceInfo& dev, NarrowPlan* plan);
 int launch_narrow(const Product& product, bool gated, const NarrowPlan& plan, const DeviceInfo& dev, cudaStream_t stream);
 
 // dz = dout act'(pre) [T, n] (pre NULL: dout), rounded once to BF16 for the products, and the sum of

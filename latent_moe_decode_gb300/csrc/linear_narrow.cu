@@ -338,30 +338,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 constexpr int room(int per_sm) { return (per_sm == 1 ? kMaxSmem : kSmSmem / per_sm) - kStaticSmem - 1024; }
 int partial_bytes(int bn, int splits) { return ((bn / 4 - 1) / splits + 1) * splits * kLanes * 16; }
 
-// Clusters of `splits` whole-SM CTAs that are resident at once (a cluster stays within a GPC, whose last SMs may be
-// too few for one more); looked up once.
-int max_clusters(int splits) {
-  static std::atomic<int> known[kMaxSplits + 1];
-  int n = known[splits].load(std::memory_order_relaxed);
-  if (n != 0) return n;
-  auto kern = linear_narrow_kernel<false>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)splits * 64);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = room(1) + 1024;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)splits, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - kStaticSmem) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
-  }
-  if (n <= 0) n = -1;
-  known[splits].store(n, std::memory_order_relaxed);
-  return n;
+// Clusters of `splits` whole-SM CTAs that are resident at once, looked up once a device; -1 where that fails.
+int max_clusters(int splits, const DeviceInfo& dev) {
+  static PerDevice<kMaxSplits + 1> known;
+  return known.get(dev.device, splits, [&] {
+    return resident_clusters(reinterpret_cast<const void*>(linear_narrow_kernel<false>), splits, kThreads, room(1) + 1024, kMaxSmem - kStaticSmem);
+  });
 }
 
 }  // namespace
@@ -373,7 +355,7 @@ int max_clusters(int splits) {
 // where 152 do; the partials, 23 ns a column (none to send: 7). Fitted to 1950 points, T 1 to 1500,
 // N 256 to 7168, K 512 to 7168, tiles of 16 to 256 rows, 1 to 8 splits: 8 % off (rms); the tile and split it
 // chooses are 2.5 % slower than the best of them on average, 14 % at most.
-NarrowPlan plan_narrow(const Product& s, bool gated, const DeviceInfo& dev) {
+int plan_narrow(const Product& s, bool gated, const DeviceInfo& dev, NarrowPlan* plan) {
   NarrowPlan best = {0, 0, 0, 1e30};
   const int nbk = (s.K - 1) / kBlockK + 1;
   const long long lane_tiles = (s.N - 1) / (gated ? kLanes / 2 : kLanes) + 1;
@@ -393,7 +375,11 @@ NarrowPlan plan_narrow(const Product& s, bool gated, const DeviceInfo& dev) {
         if (per_sm == 2 && ctas <= dev.sm_count) continue;
         if ((nbk - 1) / splits + 1 > (s.e.out_f32 ? kMaxExactRun : kMaxCutBlocks) * (512 / per_sm / bn)) continue;
         if (bn > 512 / per_sm || partial_bytes(bn, splits) > room(per_sm)) continue;
-        if (splits > 1 && tiles > (long long)per_sm * max_clusters(splits)) continue;
+        if (splits > 1) {
+          const int clusters = max_clusters(splits, dev);
+          if (clusters < 0) return MOE_ERR_CUDA;
+          if (tiles > (long long)per_sm * clusters) continue;
+        }
         if (ctas > (long long)dev.sm_count * per_sm) continue;  // (more than one wave is the wide kernel's)
         const double here = per_sm == 2 && ctas > dev.sm_count ? 2.0 : 1.0;
         const double body = here * feed / (per_sm == 2 ? 143.6 : 108.9);
@@ -404,7 +390,8 @@ NarrowPlan plan_narrow(const Product& s, bool gated, const DeviceInfo& dev) {
       }
     }
   }
-  return best;
+  *plan = best;
+  return MOE_OK;
 }
 
 namespace {

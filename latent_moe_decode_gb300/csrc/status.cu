@@ -28,6 +28,7 @@ int current_device(DeviceInfo* out) {
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_ready[dev]) {
     DeviceInfo d;
+    d.device = dev;
     if (cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&d.cc_major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&d.cc_minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||

@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "per_device.h"
 
 namespace moe {
 
@@ -133,6 +134,27 @@ struct Ring {
     if (++slot == n) slot = 0, lap ^= 1u;
   }
 };
+
+// Clusters of `ctas` CTAs of `kernel` that the current device holds at once (a cluster stays within a GPC, whose last SMs
+// may be too few for one more); -1 where the query fails.
+inline int resident_clusters(const void* kernel, int ctas, int threads, size_t smem, int max_smem) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas * 64);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  return n;
+}
 
 // The driver's tensor-map encoder (nullptr when the driver lacks it).
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
