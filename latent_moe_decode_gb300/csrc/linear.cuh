@@ -4,16 +4,13 @@
 #include <atomic>
 
 #include "activation.cuh"
+#include "narrow_shape.h"
 #include "tcgen05.cuh"
 
 namespace moe {
 namespace linear_impl {
 
 constexpr unsigned kFullMask = 0xFFFFFFFFu;
-constexpr int kMaxSmem = 227 * 1024;  // shared memory a CTA may have
-constexpr int kSmSmem = 228 * 1024;   // ... and an SM, 1 KB of it reserved per CTA
-constexpr int kStaticSmem = 1536;     // an upper bound on a kernel's static shared memory and its reserve
-constexpr int kBlockK = 64;           // K of a pipeline stage: one 128-byte swizzle row
 constexpr int kMaxCutBlocks = 128;    // of these one sum of the tensor core takes at most (8192 of K: cut off towards zero by 1e-5 of
                                       // the whole, 5e-5 where all terms have one sign; rounding to BF16 is off by up to 4e-3)
 

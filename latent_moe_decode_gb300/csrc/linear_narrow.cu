@@ -26,12 +26,7 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kWarps = kEpiWarps + 2;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLanes = 128;                    // rows of b a tile
-constexpr int kBBytes = kLanes * kBlockK * 2;  // of a stage
-constexpr int kMaxStages = 12;
-constexpr int kMaxRunBlocks = 8;               // blocks of K of a run, where TMEM has the columns
-constexpr int kMaxExactRun = 12;               // of an FP32 result, in any case (16 are off by 1e-6 of the whole)
-constexpr int kEnoughStages = 5;               // (beside the partials)
+constexpr int kMaxExactRun = 12;  // blocks of K of a run of an FP32 result, in any case (16 are off by 1e-6 of the whole)
 
 struct NarrowArgs {
   Epilogue e;
@@ -120,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     linear_narrow_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                          const __grid_constant__ NarrowArgs g, uint32_t* err) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];
+  __shared__ __align__(8) uint64_t bars[2 * kNarrowStages + 2];
   __shared__ uint32_t tmem_slot;
   const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -128,8 +123,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t partials = base + (uint32_t)(g.apart ? g.stages * (kBBytes + g.bn * kBlockK * 2) : 0);
   float* const sums = reinterpret_cast<float*>(smem_raw + (partials - raw));
   auto full = [&](int i) { return smem_u32(&bars[i]); };
-  auto empty = [&](int i) { return smem_u32(&bars[kMaxStages + i]); };
-  const uint32_t done = smem_u32(&bars[2 * kMaxStages]), came = done + 8;  // the products; the partials for this CTA
+  auto empty = [&](int i) { return smem_u32(&bars[kNarrowStages + i]); };
+  const uint32_t done = smem_u32(&bars[2 * kNarrowStages]), came = done + 8;  // the products; the partials for this CTA
   const int S = g.splits, stages = g.stages;
 
   if (threadIdx.x == 0) {
@@ -334,10 +329,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(g.tmem_cols));
 }
 
-// Shared memory of a CTA beside its alignment, where an SM holds `per_sm` of them.
-constexpr int room(int per_sm) { return (per_sm == 1 ? kMaxSmem : kSmSmem / per_sm) - kStaticSmem - 1024; }
-int partial_bytes(int bn, int splits) { return ((bn / 4 - 1) / splits + 1) * splits * kLanes * 16; }
-
 // Clusters of `splits` whole-SM CTAs that are resident at once, looked up once a device; -1 where that fails.
 int max_clusters(int splits, const DeviceInfo& dev) {
   static PerDevice<kMaxSplits + 1> known;
@@ -363,7 +354,7 @@ int plan_narrow(const Product& s, bool gated, const DeviceInfo& dev, NarrowPlan*
   const int extra = s.e.residual ? 3 : 0;  // (its loads, a thread's sixteen at a time)
   int last = 0;
   for (int most : {256, 192, 128, 96, 64, 48, 32, 16}) {
-    const int row_tiles = (s.M - 1) / most + 1, bn = ((s.M - 1) / row_tiles + 1 + 15) / 16 * 16, stage = kBBytes + bn * kBlockK * 2;
+    const int row_tiles = (s.M - 1) / most + 1, bn = ((s.M - 1) / row_tiles + 1 + 15) / 16 * 16, stage = narrow_stage_bytes(bn);
     if (bn == last) continue;
     last = bn;
     const long long tiles = ((s.M - 1) / bn + 1) * lane_tiles;
@@ -405,27 +396,8 @@ int launch(const Product& s, const NarrowPlan& plan, const DeviceInfo& dev, cuda
   const int cols = GATED ? kLanes / 2 : kLanes;
   const long long tiles = (long long)g.row_tiles * ((s.N - 1) / cols + 1);
   if (tiles >= (1LL << 31) - (1 << 16)) return MOE_ERR_CAPACITY;
-  const int blocks = (g.nbk - 1) / g.splits + 1;  // of a CTA, at most
-  g.runs = (blocks - 1) / kMaxRunBlocks + 1;
-  if (g.runs > 512 / plan.per_sm / g.bn) g.runs = 512 / plan.per_sm / g.bn;
-  g.tmem_cols = 32;
-  while (g.tmem_cols < g.runs * g.bn) g.tmem_cols *= 2;
-  // The partials stay beside the stages where enough of these are left.
-  const int stage_bytes = kBBytes + g.bn * kBlockK * 2, part = partial_bytes(g.bn, g.splits);
-  const int apart = (room(plan.per_sm) - part) / stage_bytes;
-  g.apart = apart >= kEnoughStages || apart >= blocks;
-  g.stages = g.apart ? apart : room(plan.per_sm) / stage_bytes;
-  if (g.stages > kMaxStages) g.stages = kMaxStages;
-  if (g.stages > blocks) g.stages = blocks;
-  // A CTA takes at least its TMEM columns' share of an SM's shared memory, so that the CTAs an SM holds never ask for
-  // more than its 512 columns: tcgen05.alloc would make one wait for another, in a ring of waits where clusters meet
-  // at barriers.
-  size_t smem = (size_t)g.stages * stage_bytes + (g.apart ? part : 0);
-  const size_t least = (size_t)g.tmem_cols * (kSmSmem / 512) - kStaticSmem - 1024;
-  if (smem < (size_t)part) smem = part;
-  if (smem < least) smem = least;
-  if (smem > (size_t)room(1)) smem = room(1);
-  smem += 1024;
+  const NarrowShape shape = narrow_shape(plan.bn, plan.splits, plan.per_sm, g.nbk);
+  g.stages = shape.stages, g.runs = shape.runs, g.tmem_cols = shape.tmem_cols, g.apart = shape.apart;
   CUtensorMap tm_a, tm_b;
   if (!make_map(&tm_a, s.a, s.M, s.K, g.bn)) return MOE_ERR_CUDA;
   if (!make_map(&tm_b, s.b, GATED ? 2LL * s.N : s.N, s.K, GATED ? kLanes / 2 : kLanes)) return MOE_ERR_CUDA;
@@ -435,7 +407,7 @@ int launch(const Product& s, const NarrowPlan& plan, const DeviceInfo& dev, cuda
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * g.splits));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = shape.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
