@@ -602,6 +602,8 @@ int moe_block_norm(const uint16_t* y, int64_t ldy, const void* residual, int res
  *   z   = x w^T + bias          FP32
  *   out = act(z) + residual     FP32, rounded once to out_dtype
  *   pre = z                     rounded once to BF16 (what a gradient needs of it)
+ * (An FP32 result's sum may start from the bias and, without an activation, from the residual: each
+ * run of K that is added, one per 512 of K, then rounds to FP32 with them in the sum.)
  *
  *   x         device, BF16 [T, K], rows ldx apart
  *   w         device, BF16 [N, K], rows ldw apart
@@ -630,7 +632,8 @@ int bf16_linear(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, 
  *   dx    = dz w,  dw = dz^T x  FP32 sums as bf16_linear's, rounded once to dx_dtype / dw_dtype
  *   dbias = sum_t dz[t]         FP32
  * dz goes to the products rounded once to BF16, the type they multiply (dout is BF16 already:
- * without an activation nothing is rounded), to dbias in FP32; act' within some 2^-18. Where
+ * without an activation nothing is rounded; with one, dx and dw are off by that rounding of each
+ * term, up to 2^-8 of it: 1.7e-3 of the whole, rms, in FP32 results too), to dbias in FP32; act' within some 2^-18. Where
  * a sigmoid has reached 0 or 1 its slope counts as 0, so that act'(+-infinity) is the limit.
  * relu' is 1 where z > 0 and else 0 (a NaN's too); the others' at NaN is NaN.
  *   dout       device, BF16 [T, N], rows ldd apart; pre BF16 [T, N], rows ldp apart

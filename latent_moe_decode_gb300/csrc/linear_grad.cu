@@ -1,8 +1,8 @@
 // Gradients of the BF16 products' epilogues: dz = dout act'(pre), or [dg | du] of the gated pair,
 // in BF16 for the products that follow, and the sum of dz's rows (the bias's gradient) in FP32.
 //
-// dz is rounded once to BF16, the type the tensor core multiplies; the sums are of the FP32 values
-// before that. Bound by HBM (4 bytes in and 2 out per value; gated 6 and 4).
+// dz is rounded once to BF16, the type the tensor core multiplies (the products' results are then 1.7e-3 of the
+// whole off, rms, beside their own rounding); the sums are of the FP32 values before that. Bound by HBM (4 bytes in and 2 out per value; gated 6 and 4).
 //
 // A CTA takes a strip of 64 columns, eight to a thread (16 bytes a load; where rows do not start at
 // multiples of that, every eighth column, one by one), 32 rows at a time. For the column sums the

@@ -342,10 +342,10 @@ int max_clusters(int splits, const DeviceInfo& dev) {
 // Equal tiles of the rows of a, in sixteens, K split over clusters that are all resident; two CTAs
 // an SM only where there are more of them than SMs (fewer would not be dealt out evenly). The estimate: 3.1
 // to 3.3 us of launch, first loads and end; the stages' way into an SM at 109 bytes a ns for one
-// CTA, 144 for two; all bytes at 10 TB/s (the weights partly in L2) where 304 CTAs ask for them, 6.2
-// where 152 do; the partials, 23 ns a column (none to send: 7). Fitted to 1950 points, T 1 to 1500,
+// CTA, 144 for two; all bytes at 10 TB/s (the weights partly in L2) where two CTAs an SM ask for them, 6.2
+// where one does; the partials, 23 ns a column (none to send: 7). Fitted to 1950 points, T 1 to 1500,
 // N 256 to 7168, K 512 to 7168, tiles of 16 to 256 rows, 1 to 8 splits: 8 % off (rms); the tile and split it
-// chooses are 2.5 % slower than the best of them on average, 14 % at most.
+// chooses are 2.5 % slower than the best of them on average, 14 % at most. (Without bias or activation, which it does not count.)
 int plan_narrow(const Product& s, bool gated, const DeviceInfo& dev, NarrowPlan* plan) {
   NarrowPlan best = {0, 0, 0, 1e30};
   const int nbk = (s.K - 1) / kBlockK + 1;
@@ -374,7 +374,7 @@ int plan_narrow(const Product& s, bool gated, const DeviceInfo& dev, NarrowPlan*
         if (ctas > (long long)dev.sm_count * per_sm) continue;  // (more than one wave is the wide kernel's)
         const double here = per_sm == 2 && ctas > dev.sm_count ? 2.0 : 1.0;
         const double body = here * feed / (per_sm == 2 ? 143.6 : 108.9);
-        const double stream = hbm * (1.517 - (ctas < 304 ? ctas * (0.845 / 304) : 0.845));
+        const double stream = hbm * (1.517 - 0.845 * (ctas < 2LL * dev.sm_count ? ctas / (2.0 * dev.sm_count) : 1.0));
         const double tail = splits > 1 ? here * bn * 23 - 240 : here * bn * (7.3 + extra);
         const double ns = 3320 + (body > stream ? body : stream) + tail;
         if (ns < best.ns) best = {bn, splits, per_sm, ns};

@@ -230,8 +230,8 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, int row0, int 
 }
 
 // z + bias, of which lane l holds column l of 32; z's C columns start at 16 h of them. Through shared memory,
-// 16 at a time. (FP32 results' sums start from it. 4096 x 7168 x 512, us: FP32 42, BF16 32; loaded in the epilogue
-// and handed round by 32 shuffles 49 and 33, asked for a tile ahead no less; without a bias 31 and 23.)
+// 16 at a time. (FP32 results' sums start from it. 4096 x 7168 x 512, us: FP32 42, BF16 32 to 38; loaded in the epilogue
+// and handed round by 32 shuffles 49 and 33, asked for a tile ahead no less; without a bias 32 and 23 to 26.)
 template <int C>
 __device__ __forceinline__ void add_bias(float (&z)[C], float bias, int h, float* row) {
   const int lane = threadIdx.x & 31;
@@ -674,7 +674,9 @@ WidePlan plan_wide(const Product* products, int count, bool gated, const DeviceI
   WidePlan best = {};
   // A product on `n` pairs with tiles of bn: a block of 64 of K in 168 ns at least, 51 + 0.85 bn, or its bytes at 113 a
   // ns; a tile's epilogue, by what its columns load and store, under the next tile's multiplication. (Fitted to 550
-  // points, T 1 to 1500, tiles of 64 to 256: 12 % off (rms), the choice 2.7 % slower than the best on average.)
+  // points, T 1 to 1500, tiles of 64 to 256: 12 % off (rms), the choice 2.7 % slower than the best on average. That was
+  // before the epilogue's last steps, without bias or activation, which the estimate does not count: with both an FP32
+  // gelu's time over a short K more than doubles.)
   auto time = [&](const Product& s, int bn, long long n) {
     const Epilogue& e = s.e;
     const double waves = (double)((tile_count(s, gated, bn) - 1) / n + 1);
