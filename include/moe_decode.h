@@ -617,7 +617,8 @@ int moe_block_norm(const uint16_t* y, int64_t ldy, const void* residual, int res
  * K < 2^31 - 2^16 (MOE_ERR_CAPACITY); x, w 16-byte aligned, the rest to their elements.
  * Rows that start at multiples of 16 or 32 bytes are stored in wide pieces. Sums of an FP32
  * result are taken in runs of 512 of K (to 768 for few rows, 1024 for the first two of long sums of
- * many), each rounded to nearest as it is added: within 1e-6 of the whole, rms, at K to 7168. Those of a
+ * many), each rounded to nearest as it is added: within 1e-6 of the whole, rms, at K to 7168 (2e-6
+ * where all terms have one sign). Those of a
  * BF16 result run over up to 8192 of K (what the tensor core cuts off towards zero: 1e-5 of the whole, rms, 5e-5 where all
  * terms have one sign), longer ones in runs. An activation of an FP32
  * result is evaluated to within 1e-6 of its value (0 where a sigmoid is below 2^-126; gelu's tanh form to
